@@ -1,0 +1,160 @@
+// Linear attention with one decay for each head: the forward sweeps, the
+// token-by-token steps and the plan of a call.
+#include "linattn_sweep.h"
+
+namespace linattn {
+namespace {
+
+// A few tokens (decoding): the recurrence itself in float32,
+//   M <- a M + k_t^T v_t,   o_t = is q_t M,
+// with the state's 64 columns of a block in registers: thread (x, y) holds
+// rows y, y + 16, .. of columns 4x..4x+3.  Bound by the state's bytes, read
+// and written once as whole 256-byte rows.
+template <int KX, bool BF, bool OBF>
+__global__ __launch_bounds__(NTH) void step_kernel(Sweep a, int vblocks) {
+  __shared__ float qk[2][kStepTokens][16 * KX];
+  __shared__ float part[4][64];
+  const int64_t pair = blockIdx.x / vblocks;
+  const int v0 = (int)(blockIdx.x % vblocks) * kVBlock;
+  const int64_t b = pair / a.H, h = pair % a.H;
+  const int tid = threadIdx.x, x = tid & 15, y = tid >> 4, w = tid >> 6;
+  const int n = v0 + 4 * x;
+  const bool live = n < a.V;
+  const int T = (int)tokens_of(a, b);
+  const float decay = ex2(log2_decay(a.log_decay[h]));
+
+  const auto value = [](const void* p, int64_t i) {
+    if constexpr (BF)
+      return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+    else
+      return static_cast<const float*>(p)[i];
+  };
+  float4 M[KX];
+#pragma unroll
+  for (int i = 0; i < KX; ++i) {
+    const int c = y + 16 * i;
+    M[i] = live && a.s_in && c < a.K ? *reinterpret_cast<const float4*>(a.s_in + pair * a.K * a.V + (int64_t)c * a.V + n)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int e = tid; e < T * 16 * KX; e += NTH) {
+    const int t = e / (16 * KX), c = e % (16 * KX);
+    qk[0][t][c] = c < a.K ? value(a.q.p, b * a.q.b + t * a.q.t + h * a.q.h + c) * a.is : 0.f;
+    qk[1][t][c] = c < a.K ? value(a.k.p, b * a.k.b + t * a.k.t + h * a.k.h + c) : 0.f;
+  }
+  __syncthreads();
+  for (int t = 0; t < T; ++t) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), o = v;
+    if (live) {
+      const int64_t at = b * a.v.b + t * a.v.t + h * a.v.h + n;
+      v = make_float4(value(a.v.p, at), value(a.v.p, at + 1), value(a.v.p, at + 2), value(a.v.p, at + 3));
+    }
+#pragma unroll
+    for (int i = 0; i < KX; ++i) {
+      const float k = qk[1][t][y + 16 * i], q = qk[0][t][y + 16 * i];
+      M[i].x = fmaf(decay, M[i].x, k * v.x);
+      M[i].y = fmaf(decay, M[i].y, k * v.y);
+      M[i].z = fmaf(decay, M[i].z, k * v.z);
+      M[i].w = fmaf(decay, M[i].w, k * v.w);
+      o.x = fmaf(q, M[i].x, o.x);
+      o.y = fmaf(q, M[i].y, o.y);
+      o.z = fmaf(q, M[i].z, o.z);
+      o.w = fmaf(q, M[i].w, o.w);
+    }
+    o = make_float4(wkv6::rows_sum(o.x), wkv6::rows_sum(o.y), wkv6::rows_sum(o.z), wkv6::rows_sum(o.w));
+    if ((tid & 63) < 16) *reinterpret_cast<float4*>(&part[w][4 * x]) = o;
+    __syncthreads();
+    if (tid < 64 && v0 + tid < a.V) {
+      const float r = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      const int64_t at = b * a.o.b + t * a.o.t + h * a.o.h + v0 + tid;
+      if constexpr (OBF)
+        static_cast<__bf16*>(const_cast<void*>(a.o.p))[at] = (__bf16)r;
+      else
+        static_cast<float*>(const_cast<void*>(a.o.p))[at] = r;
+    }
+    __syncthreads();
+  }
+  for (int t = T; t < (int)a.T; ++t)
+    if (tid < 64 && v0 + tid < a.V) {
+      const int64_t at = b * a.o.b + t * a.o.t + h * a.o.h + v0 + tid;
+      if constexpr (OBF)
+        static_cast<uint16_t*>(const_cast<void*>(a.o.p))[at] = 0;
+      else
+        static_cast<float*>(const_cast<void*>(a.o.p))[at] = 0.f;
+    }
+  if (a.s_out && live)
+#pragma unroll
+    for (int i = 0; i < KX; ++i) {
+      const int c = y + 16 * i;
+      if (c < a.K) *reinterpret_cast<float4*>(a.s_out + pair * a.K * a.V + (int64_t)c * a.V + n) = M[i];
+    }
+}
+
+// A call without tokens hands the state on (a kernel: a recorded memory copy
+// or clear has no place in a captured graph of the caller's).
+__global__ __launch_bounds__(NTH) void state_copy_kernel(const float4* from, float4* to, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * NTH + threadIdx.x; i < n; i += (int64_t)gridDim.x * NTH)
+    to[i] = from ? from[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <int KX>
+hipError_t launch_steps(const Sweep& a, hipStream_t s) {
+  const int vblocks = (a.V + kVBlock - 1) / kVBlock;
+  const dim3 grid((unsigned)(a.B * a.H * vblocks));
+  if (!a.bf16)
+    hipLaunchKernelGGL((step_kernel<KX, false, false>), grid, dim3(NTH), 0, s, a, vblocks);
+  else if (a.out_bf16)
+    hipLaunchKernelGGL((step_kernel<KX, true, true>), grid, dim3(NTH), 0, s, a, vblocks);
+  else
+    hipLaunchKernelGGL((step_kernel<KX, true, false>), grid, dim3(NTH), 0, s, a, vblocks);
+  return hipGetLastError();
+}
+
+bool steps(const Sweep& a) { return a.T <= kStepTokens && !a.reverse && !a.s_transposed; }
+
+SweepPlan plan(const Sweep& a) {
+  SweepPlan p;
+  p.a = a;
+  p.ws = nullptr;
+  p.vblocks = (a.V + kVBlock - 1) / kVBlock;
+  const int64_t chunks = (a.T + kChunk - 1) / kChunk, groups = a.B * a.H * p.vblocks;
+  // Two workgroups for each of the 256 CUs; segments of at least four chunks.
+  int64_t G = groups >= 256 ? 1 : (512 + groups - 1) / groups;
+  if (G > chunks / 4) G = chunks / 4;
+  if (G < 1) G = 1;
+  const int64_t per = (chunks + G - 1) / G;
+  p.seg_tokens = (int)(per * kChunk);
+  p.segments = (int)((chunks + per - 1) / per);
+  if (p.segments < 1) p.segments = 1;
+  p.items = a.B * a.H * p.segments;
+  return p;
+}
+
+}  // namespace
+
+hipError_t launch_forward(const SweepPlan& p, hipStream_t s) {
+  return p.a.K <= 64 ? launch_types<64, false>(p, s) : launch_types<128, false>(p, s);
+}
+
+hipError_t enqueue_state_copy(const float* from, float* to, int64_t n, hipStream_t s) {
+  if (from == to || n == 0) return hipSuccess;
+  const int64_t want = (n / 4 + NTH - 1) / NTH;
+  hipLaunchKernelGGL(state_copy_kernel, dim3((unsigned)(want < 4096 ? want : 4096)), dim3(NTH), 0, s,
+                     reinterpret_cast<const float4*>(from), reinterpret_cast<float4*>(to), n / 4);
+  return hipGetLastError();
+}
+
+size_t sweep_workspace_bytes(const Sweep& a) {
+  if (steps(a)) return 0;
+  const SweepPlan p = plan(a);
+  if (p.segments == 1) return 0;
+  return ((size_t)p.items * a.K * a.V * 4 + 255) / 256 * 256;
+}
+
+hipError_t enqueue_sweep(const Sweep& a, void* workspace, hipStream_t s) {
+  if (steps(a)) return a.K <= 64 ? launch_steps<4>(a, s) : launch_steps<8>(a, s);
+  SweepPlan p = plan(a);
+  if (p.segments > 1) p.ws = static_cast<float*>(workspace);
+  return a.reverse ? launch_reverse(p, s) : launch_forward(p, s);
+}
+
+}  // namespace linattn

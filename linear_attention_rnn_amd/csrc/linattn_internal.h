@@ -1,0 +1,107 @@
+// Internal interface between the C ABI layer (linattn_api.cpp) and the HIP
+// kernels of the linear-attention operators.  Not installed; not part of the
+// public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace linattn {
+
+constexpr int kChunk = 64;       // tokens of a chunk
+constexpr int kVBlock = 64;      // value channels one workgroup handles
+constexpr int kStepTokens = 8;   // calls of at most so many tokens run token by token
+
+// A [B, T, H, D] tensor: base and distances in elements (channels adjacent).
+struct Tensor {
+  const void* p;
+  int64_t b, t, h;
+};
+
+// One sweep of the recurrence over all sequences, forwards or from the last
+// token to the first.  With M the state as the sweep meets it (multiplied by
+// the decay once already where the sweep runs backwards), per token in sweep
+// order:
+//
+//   forward:   M <- a M + us k^T v;   o = q (is a M_before + ps k^T v)
+//   backward:  o = q (is M + ps k^T v);   M <- a (M + us k^T v)
+//
+// and earlier tokens of the sweep reach later ones through M.  The forward
+// operator is the forward sweep with us = 1, is = ps = scale; its gradients
+// are three sweeps over other triples of tensors.
+struct Sweep {
+  int64_t B, T, H;
+  int K, V;                 // channels of q and k; of v and o
+  Tensor q, k, v, o;
+  const float* log_decay;   // [H]
+  const int32_t* lengths;   // [B] or null
+  float us, is, ps;
+  const float* s_in;        // [B, H] states of K * V floats, or null
+  float* s_out;             // the same, or null
+  bool s_transposed;        // states are stored [V][K] (the sweep's K, V) instead of [K][V]
+  bool reverse;
+  bool bf16;                // q, k, v
+  bool out_bf16;
+};
+
+size_t sweep_workspace_bytes(const Sweep& a);
+// `workspace`: sweep_workspace_bytes(a) bytes, or null where that is 0.
+hipError_t enqueue_sweep(const Sweep& a, void* workspace, hipStream_t stream);
+
+// How a sweep is laid over the card.
+struct SweepPlan {
+  Sweep a;
+  float* ws;        // [B H][segments] entering states, [K][V]; null for one segment
+  int segments;     // of each sequence
+  int seg_tokens;   // tokens of a segment, a multiple of 64
+  int vblocks;      // blocks of 64 value channels
+  int64_t items;    // workgroups / vblocks
+};
+hipError_t launch_forward(const SweepPlan& p, hipStream_t s);
+hipError_t launch_reverse(const SweepPlan& p, hipStream_t s);
+
+// n floats from `from` (zeros where it is null) to `to`; n is a multiple of 4.
+hipError_t enqueue_state_copy(const float* from, float* to, int64_t n, hipStream_t stream);
+
+struct Rope {
+  int64_t B, T, H;
+  int D, R;
+  Tensor q, k, q_out, k_out;   // k.p null: q alone
+  const int32_t* positions;    // [B, T] or null
+  int64_t start;
+  const double* freqs;         // [R / 2]
+  bool interleaved, inverse, bf16;
+};
+hipError_t enqueue_rope(const Rope& a, hipStream_t stream);
+
+struct Norm {
+  int64_t rows, C;
+  const void* x;
+  const void* residual;   // or null
+  const float* weight;
+  float eps;
+  void* h;                // or null
+  void* y;                // normalised rows, or null with codes
+  uint8_t* codes;
+  float* scales;
+  int group;              // columns that share a scale: 128, or 0 for the row
+  bool bf16;
+};
+hipError_t enqueue_norm(const Norm& a, hipStream_t stream);
+
+struct NormBwd {
+  int64_t rows, C;
+  const void* dy;
+  const void* h;
+  const void* dh;   // or null
+  const float* weight;
+  float eps;
+  void* dx;
+  float* dweight;
+  bool bf16;
+};
+size_t norm_bwd_workspace_bytes(const NormBwd& a);
+hipError_t enqueue_norm_bwd(const NormBwd& a, void* workspace, hipStream_t stream);
+
+}  // namespace linattn

@@ -1,0 +1,380 @@
+// Root-mean-square norm of the rows of [rows, C] with the residual's addition
+// in front, an output of the inputs' type or of 8-bit codes with scales, and
+// its gradients:
+//
+//   h = x + residual (rounded to its type),  r = 1 / sqrt(mean(h^2) + eps),
+//   y = h r w;   dx = r (dy w - h r^2 mean(dy w h)) + dh,  dw = sum dy h r.
+//
+// Bound by the bytes of the rows, each read and written once: a row stays in
+// registers between its sum and its output.  TPR threads hold a row in NV
+// pieces of 8 adjacent columns each (16-byte loads of bfloat16), so a wave
+// reads 1 KiB at a time.  Sums are float32: a thread's own, then the wave's
+// by lane exchanges, then the waves' through LDS.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "linattn_internal.h"
+
+namespace linattn {
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+
+template <bool BF>
+__device__ __forceinline__ void get8(const void* p, int64_t i, float (&x)[8]) {
+  if constexpr (BF) {
+    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(u[j] << 16);
+      x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4 * j);
+      x[4 * j] = q.x;
+      x[4 * j + 1] = q.y;
+      x[4 * j + 2] = q.z;
+      x[4 * j + 3] = q.w;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pair(float a, float b) {   // bfloat16, nearest even
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+
+template <bool BF>
+__device__ __forceinline__ void put8(void* p, int64_t i, const float (&x)[8]) {
+  if constexpr (BF) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+        make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i + 4 * j) =
+          make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+  }
+}
+
+// Sum, or largest value, over the 2^k lanes that hold a group.
+template <int LANES, bool MAX>
+__device__ __forceinline__ float over_lanes(float x) {
+#pragma unroll
+  for (int m = 1; m < LANES; m *= 2) {
+    const float y = __shfl_xor(x, m, 64);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
+  return x;
+}
+
+// ... over the TPR threads of a row; `lds`: 16 floats that no one else uses.
+template <int TPR, bool MAX>
+__device__ __forceinline__ float over_row(float x, float* lds) {
+  x = over_lanes<64, MAX>(x);
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = lds[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) x = MAX ? fmaxf(x, lds[i]) : x + lds[i];
+  }
+  return x;
+}
+
+// OUT: 0 rows of the inputs' type, 1 codes with a scale per 128 columns, 2
+// codes with a scale per row.
+template <int TPR, int NV, bool BF, int OUT>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(Norm a) {
+  constexpr int NT = TPR > 256 ? TPR : 256;
+  __shared__ float lds[2][16];
+  const int at = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+  if (row >= a.rows) return;   // whole waves: TPR is a multiple of 64
+  const int64_t base = row * a.C;
+  float h[NV][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + at) * 8;
+    if (c < a.C)
+      get8<BF>(a.x, base + c, h[v]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] = 0.f;
+  }
+  if (a.residual) {
+    float r[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + at) * 8;
+      if (c < a.C)
+        get8<BF>(a.residual, base + c, r[v]);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[v][j] = 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + at) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] += r[v][j];
+      if constexpr (BF) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t u = pair(h[v][2 * j], h[v][2 * j + 1]);
+          h[v][2 * j] = __uint_as_float(u << 16);
+          h[v][2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
+        }
+      }
+      if (c < a.C) put8<BF>(a.h, base + c, h[v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(h[v][j], h[v][j], sum);
+  const float r = 1.f / sqrtf(over_row<TPR, false>(sum, lds[0]) / (float)a.C + a.eps);
+  float top = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + at) * 8;
+    float wt[8];
+    if (c < a.C) {
+      get8<false>(a.weight, c, wt);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] = h[v][j] * r * wt[j];
+    }
+    if constexpr (OUT == 0) {
+      if (c < a.C) put8<BF>(a.y, base + c, h[v]);
+    } else {
+      if constexpr (OUT == 1) top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[v][j]));
+      if constexpr (OUT == 1) {
+        // 16 lanes hold 128 adjacent columns
+        top = over_lanes<16, true>(top);
+        const float scale = top > 0.f ? top / kE4m3Max : 1.f;
+        if (c < a.C) {
+          if ((at & 15) == 0) a.scales[row * ((a.C + 127) / 128) + c / 128] = scale;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[v][j] /= scale;
+        }
+      }
+    }
+  }
+  if constexpr (OUT == 2) {
+    top = over_row<TPR, true>(top, lds[1]);
+    const float scale = top > 0.f ? top / kE4m3Max : 1.f;
+    if (at == 0) a.scales[row] = scale;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] /= scale;
+  }
+  if constexpr (OUT != 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + at) * 8;
+      if (c >= a.C) continue;
+      uint32_t q[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        int u = __builtin_amdgcn_cvt_pk_fp8_f32(h[v][4 * j], h[v][4 * j + 1], 0, false);
+        u = __builtin_amdgcn_cvt_pk_fp8_f32(h[v][4 * j + 2], h[v][4 * j + 3], u, true);
+        q[j] = (uint32_t)u;
+      }
+      *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(q[0], q[1]);
+    }
+  }
+}
+
+// ---- gradients.  A workgroup walks over rows a grid apart and keeps its
+// columns' sums of dy h r in registers; the workgroups' sums go to the
+// workspace and are added up in the order of the workgroups.
+template <int TPR, int NV, bool BF>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd a, float* part) {
+  constexpr int NT = TPR > 256 ? TPR : 256, RW = NT / TPR;
+  __shared__ float lds[2][2][16];
+  __shared__ float join[RW > 1 ? TPR * NV * 8 : 1];
+  const int at = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  float dw[NV][8], wt[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + at) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[v][j] = wt[v][j] = 0.f;
+    if (c < a.C) get8<false>(a.weight, c, wt[v]);
+  }
+  int turn = 0;
+  // every wave of a workgroup makes the same turns where rows are shared by waves (RW == 1)
+  for (int64_t row = (int64_t)blockIdx.x * RW + slot; row < a.rows; row += (int64_t)gridDim.x * RW, turn ^= 1) {
+    const int64_t base = row * a.C;
+    float h[NV][8], d[NV][8];
+    float hh = 0.f, hd = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + at) * 8;
+      if (c < a.C) {
+        get8<BF>(a.h, base + c, h[v]);
+        get8<BF>(a.dy, base + c, d[v]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[v][j] = d[v][j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hh = fmaf(h[v][j], h[v][j], hh);
+        hd = fmaf(h[v][j], d[v][j] * wt[v][j], hd);
+      }
+    hh = over_row<TPR, false>(hh, lds[turn][0]);
+    hd = over_row<TPR, false>(hd, lds[turn][1]);
+    const float r = 1.f / sqrtf(hh / (float)a.C + a.eps);
+    const float f = r * r * (hd / (float)a.C);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + at) * 8;
+      if (c >= a.C) continue;
+      float x[8];
+      if (a.dh)
+        get8<BF>(a.dh, base + c, x);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[v][j] = fmaf(d[v][j], h[v][j] * r, dw[v][j]);
+        x[j] = fmaf(r, d[v][j] * wt[v][j] - h[v][j] * f, x[j]);
+      }
+      put8<BF>(a.dx, base + c, x);
+    }
+  }
+  if constexpr (RW > 1) {
+    for (int s = 0; s < RW; ++s) {
+      if (slot == s)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float& q = join[(v * 8 + j) * TPR + at];
+            q = s == 0 ? dw[v][j] : q + dw[v][j];
+          }
+      __syncthreads();
+    }
+    if (slot == 0)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[v][j] = join[(v * 8 + j) * TPR + at];
+  }
+  if (slot == 0)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + at) * 8;
+      if (c < a.C) put8<false>(part, blockIdx.x * a.C + c, dw[v]);
+    }
+}
+
+// dweight[c] = the workgroups' sums, in 16 interleaved shares.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, float* dweight, int groups, int64_t C) {
+  __shared__ float lds[16][65];
+  const int c = threadIdx.x % 64, s = threadIdx.x / 64;
+  const int64_t col = (int64_t)blockIdx.x * 64 + c;
+  float x = 0.f;
+  if (col < C)
+    for (int i = s; i < groups; i += 16) x += part[i * C + col];
+  lds[s][c] = x;
+  __syncthreads();
+  if (s == 0 && col < C) {
+    for (int i = 1; i < 16; ++i) x += lds[i][c];
+    dweight[col] = x;
+  }
+}
+
+// Threads of a row and pieces of each, at most four (32 columns a thread: two
+// rows of them and the gradient's sums fit the registers): a wave holds up to
+// 2048 columns, four waves 8192, eight the rest; where rows are few, four
+// waves share rows of more than 512 columns, for a wave alone would wait for
+// its loads.
+struct Shape {
+  int tpr, nv;
+};
+Shape shape_of(int64_t rows, int64_t C) {
+  const int64_t pieces = C / 8;
+  const int tpr = pieces <= 64 || (pieces <= 256 && rows >= 2048) ? 64 : pieces <= 1024 ? 256 : 512;
+  const int64_t need = (pieces + tpr - 1) / tpr;
+  return {tpr, need <= 1 ? 1 : need <= 2 ? 2 : 4};
+}
+
+template <int TPR, int NV>
+void launch_norm(const Norm& a, hipStream_t s) {
+  constexpr int NT = TPR > 256 ? TPR : 256;
+  const dim3 grid((unsigned)((a.rows + NT / TPR - 1) / (NT / TPR)));
+  const int out = !a.codes ? 0 : a.group ? 1 : 2;
+  auto* k = a.bf16 ? (out == 0 ? norm_kernel<TPR, NV, true, 0> : out == 1 ? norm_kernel<TPR, NV, true, 1> : norm_kernel<TPR, NV, true, 2>)
+                   : (out == 0 ? norm_kernel<TPR, NV, false, 0> : out == 1 ? norm_kernel<TPR, NV, false, 1> : norm_kernel<TPR, NV, false, 2>);
+  hipLaunchKernelGGL(k, grid, dim3(NT), 0, s, a);
+}
+
+template <int TPR, int NV>
+void launch_norm_bwd(const NormBwd& a, float* part, int groups, hipStream_t s) {
+  constexpr int NT = TPR > 256 ? TPR : 256;
+  auto* k = a.bf16 ? norm_bwd_kernel<TPR, NV, true> : norm_bwd_kernel<TPR, NV, false>;
+  hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(NT), 0, s, a, part);
+}
+
+// Workgroups of the gradients: two for each CU, never more than there are
+// rows for them.
+int bwd_groups(const NormBwd& a, const Shape& f) {
+  const int rw = f.tpr >= 256 ? 1 : 4;
+  const int64_t want = (a.rows + rw - 1) / rw;
+  return (int)(want < 512 ? want : 512);
+}
+
+}  // namespace
+
+// call(TPR, NV) for the shape f (512 threads: more than 8192 columns)
+#define LINATTN_SHAPES(call)             \
+  if (f.tpr == 64) {                     \
+    if (f.nv == 1) call(64, 1);          \
+    else if (f.nv == 2) call(64, 2);     \
+    else call(64, 4);                    \
+  } else if (f.tpr == 256) {             \
+    if (f.nv == 1) call(256, 1);         \
+    else if (f.nv == 2) call(256, 2);    \
+    else call(256, 4);                   \
+  } else {                               \
+    call(512, 4);                        \
+  }
+
+hipError_t enqueue_norm(const Norm& a, hipStream_t s) {
+  const Shape f = shape_of(a.rows, a.C);
+#define LINATTN_CALL(T, N) launch_norm<T, N>(a, s)
+  LINATTN_SHAPES(LINATTN_CALL)
+#undef LINATTN_CALL
+  return hipGetLastError();
+}
+
+size_t norm_bwd_workspace_bytes(const NormBwd& a) { return (size_t)bwd_groups(a, shape_of(a.rows, a.C)) * a.C * 4; }
+
+hipError_t enqueue_norm_bwd(const NormBwd& a, void* workspace, hipStream_t s) {
+  const Shape f = shape_of(a.rows, a.C);
+  const int groups = bwd_groups(a, f);
+  float* part = static_cast<float*>(workspace);
+  if (groups) {
+#define LINATTN_CALL(T, N) launch_norm_bwd<T, N>(a, part, groups, s)
+    LINATTN_SHAPES(LINATTN_CALL)
+#undef LINATTN_CALL
+  }
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.C + 63) / 64)), dim3(1024), 0, s, part, a.dweight, groups, a.C);
+  return hipGetLastError();
+}
+
+}  // namespace linattn

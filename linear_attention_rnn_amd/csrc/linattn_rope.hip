@@ -1,0 +1,161 @@
+// Rotary positions of queries and keys: pair i of a head's first R channels
+// is turned by position * freqs[i],  (x, y) -> (x cos - y sin, x sin + y cos).
+//
+// Bound by the bytes of q and k, read and written once.  The angles of a
+// token are the same for all its heads, so a workgroup takes a few tokens,
+// puts the cosines and sines of their R / 2 angles into LDS and then streams
+// all heads of q and k past them, 16 bytes a load.
+//
+// Angles are products of whole positions and float64 frequencies, reduced to
+// a part of a turn before they are rounded to float32: the quotient by 2 pi is
+// formed with its rounding error (two products), its nearest quarter turn is
+// taken off exactly, and what is left, at most an eighth of a turn, loses
+// 2^-24 of itself.  A position of 10^9 is as exact as one of 10.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "linattn_internal.h"
+
+namespace linattn {
+namespace {
+
+constexpr int NTR = 256;
+constexpr int kMaxAngles = 1024;   // tokens of a workgroup times R / 2
+
+__device__ __forceinline__ float2 turn_of(double angle, bool inverse) {
+  constexpr double kInv2Pi = 0.15915494309189535;       // 1 / (2 pi), rounded
+  constexpr double kInv2PiLow = -9.839338337591243e-18;  // and what the rounding left
+  const double t = angle * kInv2Pi, low = fma(angle, kInv2Pi, -t) + angle * kInv2PiLow;
+  const double k = rint(4.0 * t);
+  const float f = (float)(fma(-0.25, k, t) + low);
+  float s, c;
+  sincospif(2.f * f, &s, &c);
+  const int q = (int)(k - 4.0 * floor(0.25 * k));
+  const float cs = q & 1 ? s : c, sn = q & 1 ? c : s;
+  const float co = q == 1 || q == 2 ? -cs : cs, si = q >= 2 ? -sn : sn;
+  return make_float2(co, inverse ? -si : si);
+}
+
+__device__ __forceinline__ uint32_t pair(float a, float b) {   // bfloat16, nearest even
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+
+// N adjacent values as one or two loads or stores of up to 16 bytes.
+template <bool BF, int N>
+__device__ __forceinline__ void get(const void* p, int64_t i, float (&x)[N]) {
+  constexpr int Z = BF ? 2 : 4, W = N * Z / 4 > 0 ? N * Z / 4 : 1;
+  uint32_t u[W];
+  const char* at = static_cast<const char*>(p) + i * Z;
+  if constexpr (N * Z == 2)
+    u[0] = *reinterpret_cast<const uint16_t*>(at);
+  else
+    __builtin_memcpy(u, __builtin_assume_aligned(at, N * Z > 16 ? 16 : N * Z), N * Z);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    x[j] = BF ? __uint_as_float(j % 2 ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16) : __uint_as_float(u[BF ? 0 : j]);
+}
+
+template <bool BF, int N>
+__device__ __forceinline__ void put(void* p, int64_t i, const float (&x)[N]) {
+  constexpr int Z = BF ? 2 : 4, W = N * Z / 4 > 0 ? N * Z / 4 : 1;
+  uint32_t u[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) u[j] = BF ? pair(x[2 * j < N ? 2 * j : 0], x[2 * j + 1 < N ? 2 * j + 1 : 0]) : __float_as_uint(x[j]);
+  char* at = static_cast<char*>(p) + i * Z;
+  if constexpr (N * Z == 2)
+    *reinterpret_cast<uint16_t*>(at) = (uint16_t)u[0];
+  else
+    __builtin_memcpy(__builtin_assume_aligned(at, N * Z > 16 ? 16 : N * Z), u, N * Z);
+}
+
+// blockIdx.x: a group of `tokens` tokens; blockIdx.y: a share of the rows
+// (tensor, head) of each token.  A piece is N adjacent channels: N / 2 pairs
+// in place (interleaved), or N pairs whose halves lie R / 2 apart; N divides
+// what a piece must not cross (R, or R / 2).
+template <bool BF, bool INTER, int N>
+__global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens, int rows_share) {
+  __shared__ float2 cs[kMaxAngles];
+  const int half = a.R / 2, tid = threadIdx.x;
+  const int64_t n = a.B * a.T, first = (int64_t)blockIdx.x * tokens;
+  const int nt = (int)(n - first < tokens ? n - first : tokens);
+  for (int e = tid; e < nt * half; e += NTR) {
+    const int64_t tok = first + e / half;
+    const int64_t pos = a.start + (a.positions ? (int64_t)a.positions[tok] : tok % a.T);
+    cs[e] = turn_of((double)pos * a.freqs[e % half], a.inverse);
+  }
+  __syncthreads();
+  // pieces of a row: those that turn, then those that are copied
+  const int turning = INTER ? a.R / N : half / N, units = turning + (a.D - a.R) / N;
+  const int per = NTR / units, u = tid % units, slot = tid / units;
+  if (slot >= per) return;
+  const int all = a.k.p ? 2 * (int)a.H : (int)a.H, r0 = blockIdx.y * rows_share;
+  const int rows = all - r0 < rows_share ? all - r0 : rows_share;
+  for (int row = slot; row < nt * rows; row += per) {
+    const int ti = row / rows, r = r0 + row % rows;
+    const int64_t tok = first + ti, b = tok / a.T, t = tok % a.T;
+    const bool isk = r >= a.H;
+    const int64_t h = isk ? r - a.H : r;
+    const Tensor& x = isk ? a.k : a.q;
+    const Tensor& y = isk ? a.k_out : a.q_out;
+    const int64_t from = b * x.b + t * x.t + h * x.h, to = b * y.b + t * y.t + h * y.h;
+    void* out = const_cast<void*>(y.p);
+    float p[N], q[N];
+    if (u >= turning) {
+      const int c = a.R + N * (u - turning);
+      get<BF>(x.p, from + c, p);
+      put<BF>(out, to + c, p);
+    } else if constexpr (INTER) {
+      get<BF>(x.p, from + N * u, p);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 e = cs[ti * half + N / 2 * u + j];
+        const float v = p[2 * j], z = p[2 * j + 1];
+        p[2 * j] = v * e.x - z * e.y;
+        p[2 * j + 1] = v * e.y + z * e.x;
+      }
+      put<BF>(out, to + N * u, p);
+    } else {
+      get<BF>(x.p, from + N * u, p);
+      get<BF>(x.p, from + half + N * u, q);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float2 e = cs[ti * half + N * u + j];
+        const float v = p[j];
+        p[j] = v * e.x - q[j] * e.y;
+        q[j] = v * e.y + q[j] * e.x;
+      }
+      put<BF>(out, to + N * u, p);
+      put<BF>(out, to + half + N * u, q);
+    }
+  }
+}
+
+template <bool BF, bool INTER>
+auto kernel_for(const Rope& a) {
+  const int fit = INTER ? a.R : a.R / 2;   // R is even, D a multiple of 8
+  return fit % 8 == 0 ? rope_kernel<BF, INTER, 8> : fit % 4 == 0 ? rope_kernel<BF, INTER, 4> : rope_kernel<BF, INTER, INTER ? 2 : 1>;
+}
+
+}  // namespace
+
+hipError_t enqueue_rope(const Rope& a, hipStream_t s) {
+  const int64_t n = a.B * a.T;
+  const int64_t rows = a.k.p ? 2 * a.H : a.H;
+  // Sixteen tokens a workgroup, fewer where the angles would not fit or the
+  // card would not be filled; a token's rows are shared out if there are few.
+  int tokens = 16;
+  while (tokens > 1 && (tokens * (a.R / 2) > kMaxAngles || n / tokens < 1024)) tokens /= 2;
+  int64_t shares = 1;
+  const int64_t groups = (n + tokens - 1) / tokens;
+  while (groups * shares < 512 && rows / (2 * shares) >= 8) shares *= 2;
+  const int share = (int)((rows + shares - 1) / shares);
+  const dim3 grid((unsigned)groups, (unsigned)((rows + share - 1) / share));
+  auto* kernel = a.bf16 ? (a.interleaved ? kernel_for<true, true>(a) : kernel_for<true, false>(a))
+                        : (a.interleaved ? kernel_for<false, true>(a) : kernel_for<false, false>(a));
+  hipLaunchKernelGGL(kernel, grid, dim3(NTR), 0, s, a, tokens, share);
+  return hipGetLastError();
+}
+
+}  // namespace linattn

@@ -1,0 +1,447 @@
+// Linear attention with one decay for each head: the chunked sweep on matrix
+// cores and its segment carries.  Included by the two files that instantiate
+// it (linattn_forward.hip,
+// linattn_reverse.hip).
+//
+// Mathematics, for a chunk of n <= 64 tokens in sweep order with the state M
+// (K x V) entering it, a the decay, d = 0 for the forward sweep and 1 for the
+// reversed one (whose state carries one decay more):
+//
+//   o_j = is a^(j+1-d) q_j M  +  sum_{i<=j} ps a^(j-i) (q_j . k_i) v_i
+//   M  <- a^n M  +  sum_i k_i^T (us a^(n-1-i+d) v_i)
+//
+// All exponents are >= 0, so every factor is at most 1 for a decay a <= 1.
+//
+// A workgroup of four waves runs one (batch item, head, block of 64 value
+// channels, segment).  Wave w computes the outputs of tokens 16w..16w+15 (all
+// 64 channels, transposed: O^T[n][t]) and keeps the state's columns of its
+// strip of 16 value channels in registers.  MFMA operands chain without a
+// detour: scores come out as K Q^T tiles whose accumulator lanes are, tile
+// pairs taken together, the operand lanes of the product with V^T; the state's
+// accumulators are the operand lanes of the product with q.  Only the state
+// crosses waves, through LDS as ready-made operand fragments.
+//
+// The rows of an MFMA tile may be any 16 channels as long as both sides of a
+// product agree: "tile pairs" (2u, 2u+1) hold channels 32u + 8(m/4) + m%4 and
+// those + 4 in row m, so that a lane's values of both tiles are 8 adjacent
+// channels: a 16-byte operand of q, and 16-byte stores of bfloat16 outputs.
+//
+// Operand parts: bfloat16 inputs are one part, float32 inputs three.  MP parts
+// carry what arises in between (scores times decays, the state as it meets
+// q): one where the output is bfloat16 too (each adds a rounding of the size
+// of the output's own, 2^-8, to the part of the output it carries), three
+// where it is float32.  UP parts carry the decayed values of the state's
+// update: two (2^-16) where the state ends in bfloat16 outputs alone, three
+// where it is handed back or read at float32.
+#pragma once
+
+#include "linattn_internal.h"
+#include "wkv6_device.h"
+
+namespace linattn {
+namespace {
+
+using wkv6::bf16x4;
+using wkv6::bf16x8;
+using wkv6::ex2;
+using wkv6::f32x4;
+using wkv6::ld_tr;
+using wkv6::lds_barrier;
+using wkv6::mma;
+using wkv6::Op;
+using wkv6::Rsrc;
+using wkv6::swz;
+
+constexpr int NTH = 256;
+constexpr int kPlane = 64 * 64;
+
+// log2 of the decay, finite: the factor of any distance > 0 is 0 at -4096.
+__device__ __forceinline__ float log2_decay(float ld) { return ld < -2839.f ? -4096.f : ld * 1.44269504f; }
+
+__device__ __forceinline__ int64_t tokens_of(const Sweep& a, int64_t b) {
+  if (!a.lengths) return a.T;
+  const int64_t n = a.lengths[b];
+  return n < 0 ? 0 : n > a.T ? a.T : n;
+}
+
+// The rows of one chunk of a tensor: nt rows from token a0 on.
+__device__ __forceinline__ Rsrc chunk_rsrc(const Tensor& x, int64_t b, int64_t h, int64_t a0, int nt, int D, int isz) {
+  char* base = static_cast<char*>(const_cast<void*>(x.p)) + (b * x.b + h * x.h + a0 * x.t) * isz;
+  return __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)(((nt - 1) * x.t + D) * isz), wkv6::kRsrcFlags);
+}
+
+// Eight adjacent channels as loaded: 16 bytes of bfloat16 or 32 of float32.
+template <bool BF>
+struct Raw8 {
+  uint4 q[BF ? 1 : 2];
+};
+
+template <bool BF>
+__device__ __forceinline__ Raw8<BF> load8(Rsrc r, int off) {
+  Raw8<BF> x;
+  x.q[0] = wkv6::bload16(r, off);
+  if constexpr (!BF) x.q[1] = wkv6::bload16(r, off + 16);
+  return x;
+}
+
+template <bool BF>
+__device__ __forceinline__ Op<BF ? 1 : 3> operand(const Raw8<BF>& x) {
+  if constexpr (BF) {
+    Op<1> o;
+    o.p[0] = __builtin_bit_cast(bf16x8, x.q[0]);
+    return o;
+  } else {
+    float f[8];
+    __builtin_memcpy(f, x.q, 32);
+    return wkv6::split8<3, false>(f);
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ void stage8(__bf16* plane, int stride, int off, const Raw8<BF>& x) {
+  const Op<BF ? 1 : 3> o = operand<BF>(x);
+#pragma unroll
+  for (int s = 0; s < (BF ? 1 : 3); ++s) *reinterpret_cast<bf16x8*>(plane + s * stride + off) = o.p[s];
+}
+
+template <int S>
+__device__ __forceinline__ Op<S> read8(const __bf16* p, int stride, int off) {
+  Op<S> o;
+#pragma unroll
+  for (int s = 0; s < S; ++s) o.p[s] = *reinterpret_cast<const bf16x8*>(p + s * stride + off);
+  return o;
+}
+
+// Two transposed reads: slots 0..3 from the rows of `o0`, 4..7 from those of `o1`.
+template <int S>
+__device__ __forceinline__ Op<S> read_tr(const __bf16* p, int stride, int o0, int o1) {
+  Op<S> o;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const bf16x4 a = ld_tr(p + s * stride + o0), b = ld_tr(p + s * stride + o1);
+    o.p[s] = bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  }
+  return o;
+}
+
+template <int KP, bool BF, int MP, int UP, bool REV, bool OBF, bool SUMMARY>
+__global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
+  constexpr int NI = BF ? 1 : 3;             // parts of an input operand
+  constexpr int ISZ = BF ? 2 : 4;
+  constexpr int NJ = KP / 32;                // groups of 32 key channels
+  constexpr int KPL = (KP / 64) * kPlane;    // one part of the keys
+  constexpr int KR = KP / 32;                // key chunks of 8 channels a thread loads
+  __shared__ __bf16 Kp[NI * KPL];
+  __shared__ __bf16 Vp[NI * kPlane];
+  __shared__ __bf16 Sp[SUMMARY ? 8 : MP * KP * 64];
+
+  const Sweep& a = p.a;
+  // Blocks of one item are 8 apart, so that they run on one XCD and share its L2.
+  const int64_t item = (int64_t)(blockIdx.x / (8 * p.vblocks)) * 8 + blockIdx.x % 8;
+  const int vb = (blockIdx.x / 8) % p.vblocks;
+  if (item >= p.items) return;
+  const int segs = SUMMARY ? p.segments - 1 : p.segments;
+  const int64_t pair = item / segs;
+  const int seg = (int)(item % segs);
+  const int64_t b = pair / a.H, h = pair % a.H;
+  const int v0 = vb * kVBlock;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const float gl = log2_decay(a.log_decay[h]);
+
+  const int64_t len = tokens_of(a, b);
+  const int64_t lo = (int64_t)seg * p.seg_tokens;
+  const int64_t hi = lo + p.seg_tokens < len ? lo + p.seg_tokens : len;
+  const int nch = lo < hi ? (int)((hi - lo + kChunk - 1) / kChunk) : 0;
+
+  // ---- the entering state: rows c = 32J + 8g + 4e + r, column n of strip w
+  f32x4 M[NJ][2];
+  const int sn = v0 + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
+  const float* s_from = nullptr;
+  int64_t cs = a.V, ns = 1;
+  if constexpr (!SUMMARY) {
+    if (p.ws)
+      s_from = p.ws + (pair * p.segments + seg) * a.K * a.V;
+    else if (a.s_in) {
+      s_from = a.s_in + pair * a.K * a.V;
+      if (a.s_transposed) cs = 1, ns = a.K;
+    }
+  }
+#pragma unroll
+  for (int J = 0; J < NJ; ++J)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int c = 32 * J + 8 * g + 4 * e + r;
+        M[J][e][r] = s_from && c < a.K && sn < a.V ? s_from[c * cs + sn * ns] : 0.f;
+      }
+
+  // ---- factors of whole chunks
+  const float f_inter = ex2(gl * (16 * w + li + (REV ? 0 : 1))) * a.is;   // column t = 16w + li
+  float dg[4], of[4];   // tile of the wave's own tokens; the tile before it
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int d = li - 4 * g - r;
+    dg[r] = d >= 0 ? ex2(gl * d) * a.ps : 0.f;
+    of[r] = ex2(gl * (16 + d)) * a.ps;
+  }
+  const float a16 = ex2(gl * 16.f);
+  float uf[2][8];   // tokens 32u + 8g + j in the state's update
+  const auto update_factors = [&](int nt) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int d = nt - 1 + (REV ? 1 : 0) - (32 * u + 8 * g + j);
+        uf[u][j] = d >= 0 ? ex2(gl * d) * a.us : 0.f;
+      }
+  };
+  update_factors(kChunk);
+
+  // ---- loads: chunk c covers nt tokens from a0 on; row j in sweep order
+  Raw8<BF> kr[KR], vr[2], qr[NJ];
+  const auto load = [&](int c) {
+    const int64_t at = lo + (int64_t)c * kChunk;
+    const int nt = (int)(hi - at < kChunk ? hi - at : kChunk);
+    const int64_t a0 = REV ? len - at - nt : at;
+    const Rsrc rk = chunk_rsrc(a.k, b, h, a0, nt, a.K, ISZ), rv = chunk_rsrc(a.v, b, h, a0, nt, a.V, ISZ);
+    const auto off = [&](int j, int64_t stride, int col, int D) {
+      return j < nt && col < D ? (REV ? nt - 1 - j : j) * (int)stride * ISZ + col * ISZ : wkv6::kOffNone;
+    };
+#pragma unroll
+    for (int x = 0; x < KR; ++x) {
+      const int id = tid + x * NTH;
+      kr[x] = load8<BF>(rk, off(id / (KP / 8), a.k.t, id % (KP / 8) * 8, a.K));
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int id = tid + x * NTH;
+      vr[x] = load8<BF>(rv, off(id / 8, a.v.t, v0 + id % 8 * 8, a.V));
+    }
+    if constexpr (!SUMMARY) {
+      const Rsrc rq = chunk_rsrc(a.q, b, h, a0, nt, a.K, ISZ);
+#pragma unroll
+      for (int J = 0; J < NJ; ++J) qr[J] = load8<BF>(rq, off(16 * w + li, a.q.t, 32 * J + 8 * g, a.K));
+    }
+  };
+  if (nch > 0) load(0);
+
+  const bool last_seg = hi == len;
+  for (int c = 0; c < nch; ++c) {
+    const int64_t at = lo + (int64_t)c * kChunk;
+    const int nt = (int)(hi - at < kChunk ? hi - at : kChunk);
+    const int64_t a0 = REV ? len - at - nt : at;
+    // ---- keys, values and the state to LDS
+#pragma unroll
+    for (int x = 0; x < KR; ++x) {
+      const int id = tid + x * NTH, row = id / (KP / 8), c8 = id % (KP / 8);
+      stage8<BF>(Kp + (c8 >> 3) * kPlane, KPL, swz(row, (c8 & 7) * 8), kr[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int id = tid + x * NTH;
+      stage8<BF>(Vp, kPlane, swz(id / 8, id % 8 * 8), vr[x]);
+    }
+    Op<NI> qf[NJ];
+    if constexpr (!SUMMARY) {
+#pragma unroll
+      for (int J = 0; J < NJ; ++J) {
+        qf[J] = operand<BF>(qr[J]);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = M[J][e >> 2][e & 3];
+        const Op<MP> o = wkv6::split8<MP, false>(f);
+#pragma unroll
+        for (int s = 0; s < MP; ++s)
+          *reinterpret_cast<bf16x8*>(Sp + ((s * 4 + w) * NJ + J) * 512 + lane * 8) = o.p[s];
+      }
+    }
+    lds_barrier();
+    if (c + 1 < nch) load(c + 1);
+
+    if constexpr (!SUMMARY) {
+      if (16 * w < nt) {
+        // ---- the state's part: O^T[n][t] = sum_c M[c][n] q_t[c]
+        f32x4 acc[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int J = 0; J < NJ; ++J)
+            acc[s] = mma<MP, NI>(read8<MP>(Sp, 4 * NJ * 512, (s * NJ + J) * 512 + lane * 8), qf[J], acc[s]);
+          acc[s] *= f_inter;
+        }
+        // ---- the chunk's own part, two tiles of 16 tokens i at a time
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (2 * u <= w) {
+            float pr[8];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int I = 2 * u + e;
+              f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+              if (I <= w) {
+#pragma unroll
+                for (int J = 0; J < NJ; ++J)
+                  sc = mma<NI, NI>(read8<NI>(Kp + (J >> 1) * kPlane, KPL, swz(16 * I + li, 32 * (J & 1) + 8 * g)), qf[J], sc);
+                const float far = I + 2 == w ? a16 : I + 3 == w ? a16 * a16 : 1.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sc[r] *= I == w ? dg[r] : of[r] * far;
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) pr[4 * e + r] = sc[r];
+            }
+            const Op<MP> pf = wkv6::split8<MP, false>(pr);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const int row = 32 * u + 4 * g + (li >> 2), col = 4 * (s >> 1) + (li & 3);
+              const Op<NI> vf = read_tr<NI>(Vp, kPlane, row * 64 + ((col ^ (row & 7)) << 3) + 4 * (s & 1),
+                                            (row + 16) * 64 + ((col ^ (row & 7)) << 3) + 4 * (s & 1));
+              acc[s] = mma<NI, MP>(vf, pf, acc[s]);
+            }
+          }
+        }
+        // ---- store: row t, channels v0 + 32u + 8g..+7
+        const int j = 16 * w + li;
+        constexpr int OSZ = OBF ? 2 : 4;
+        const Rsrc ro = chunk_rsrc(a.o, b, h, a0, nt, a.V, OSZ);
+        const int orow = (REV ? nt - 1 - j : j) * (int)a.o.t;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int n = v0 + 32 * u + 8 * g;
+          const int off = j < nt && n < a.V ? (orow + n) * OSZ : wkv6::kOffNone;
+          const f32x4 x = acc[2 * u], y = acc[2 * u + 1];
+          if constexpr (OBF) {
+            typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+            const u32x4 q = {__builtin_bit_cast(unsigned int, wkv6::round_pair(x[0], x[1])),
+                             __builtin_bit_cast(unsigned int, wkv6::round_pair(x[2], x[3])),
+                             __builtin_bit_cast(unsigned int, wkv6::round_pair(y[0], y[1])),
+                             __builtin_bit_cast(unsigned int, wkv6::round_pair(y[2], y[3]))};
+            __builtin_amdgcn_raw_buffer_store_b128(q, ro, off, 0, 0);
+          } else {
+            wkv6::bstoref4(ro, off, x[0], x[1], x[2], x[3]);
+            wkv6::bstoref4(ro, off + 16, y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+    }
+
+    // ---- the state's update
+    if (SUMMARY || c + 1 < nch || (a.s_out && last_seg)) {
+      if (nt < kChunk) update_factors(nt);
+      const float an = ex2(gl * nt);
+#pragma unroll
+      for (int J = 0; J < NJ; ++J)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) M[J][e] *= an;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (32 * u < nt) {
+          const int row = 32 * u + 8 * g + (li >> 2);   // and + 4
+          const auto at_col = [&](int col, int half, int add) {
+            return (row + add) * 64 + ((col ^ ((row + add) & 7)) << 3) + 4 * half;
+          };
+          const int vc = 4 * (w >> 1) + (li & 3);
+          const Op<NI> vo = read_tr<NI>(Vp, kPlane, at_col(vc, w & 1, 0), at_col(vc, w & 1, 4));
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            f[j] = (float)vo.p[0][j];
+            if constexpr (NI == 3) f[j] += (float)vo.p[1][j] + (float)vo.p[2][j];
+            f[j] *= uf[u][j];
+          }
+          const Op<UP> vf = wkv6::split8<UP, false>(f);
+#pragma unroll
+          for (int J = 0; J < NJ; ++J)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int kc = 4 * (J & 1) + (li & 3);
+              M[J][e] = mma<NI, UP>(read_tr<NI>(Kp + (J >> 1) * kPlane, KPL, at_col(kc, e, 0), at_col(kc, e, 4)), vf, M[J][e]);
+            }
+        }
+      }
+    }
+    lds_barrier();
+  }
+
+  // ---- hand on the state
+  float* s_to = nullptr;
+  if constexpr (SUMMARY)
+    s_to = p.ws + (pair * p.segments + seg) * a.K * a.V;
+  else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
+    s_to = a.s_out + pair * a.K * a.V;
+    cs = a.s_transposed ? 1 : a.V;
+    ns = a.s_transposed ? a.K : 1;
+  }
+  if (s_to)
+#pragma unroll
+    for (int J = 0; J < NJ; ++J)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int c = 32 * J + 8 * g + 4 * e + r;
+          if (c < a.K && sn < a.V) s_to[c * cs + sn * ns] = M[J][e][r];
+        }
+
+  // ---- rows behind the sequence: zero, each segment those of its own places
+  if constexpr (!SUMMARY) {
+    const int64_t z0 = len > lo ? len : lo, z1 = lo + p.seg_tokens < a.T ? lo + p.seg_tokens : a.T;
+    constexpr int OSZ = OBF ? 2 : 4;
+    for (int64_t t = z0 + tid / 8; t < z1; t += NTH / 8) {
+      const int n = v0 + tid % 8 * 8;
+      if (n < a.V) {
+        char* q = static_cast<char*>(const_cast<void*>(a.o.p)) + (b * a.o.b + h * a.o.h + t * a.o.t + n) * OSZ;
+#pragma unroll
+        for (int x = 0; x < OSZ / 2; ++x) reinterpret_cast<uint4*>(q)[x] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+}
+
+// The segments' own states, as the summaries left them, become the states
+// that enter the segments: M_0 = s_in, M_{s+1} = a^(tokens of s) M_s + U_s.
+__global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
+  const Sweep& a = p.a;
+  const int64_t pair = blockIdx.x;
+  const int e = blockIdx.y * NTH + threadIdx.x, KV = a.K * a.V;
+  if (e >= KV) return;
+  const int64_t len = tokens_of(a, pair / a.H);
+  const float gl = log2_decay(a.log_decay[pair % a.H]);
+  const int from = a.s_transposed ? (e % a.V) * a.K + e / a.V : e;
+  float m = a.s_in ? a.s_in[pair * KV + from] : 0.f;
+  float* at = p.ws + pair * p.segments * KV + e;
+  for (int s = 0; s < p.segments; ++s, at += KV) {
+    const float u = s + 1 < p.segments ? *at : 0.f;
+    *at = m;
+    const int64_t lo = (int64_t)s * p.seg_tokens, left = len - lo;
+    const int64_t n = left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens;
+    m = m * ex2(gl * (float)n) + u;
+  }
+}
+
+template <int KP, bool BF, int MP, int UP, bool REV, bool OBF>
+hipError_t launch(SweepPlan p, hipStream_t s) {
+  const int64_t pairs = p.a.B * p.a.H;
+  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.vblocks)); };
+  if (p.segments > 1) {
+    SweepPlan q = p;
+    q.items = pairs * (p.segments - 1);
+    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, REV, OBF, true>), grid(q.items), dim3(NTH), 0, s, q);
+    hipLaunchKernelGGL(carry_kernel, dim3((unsigned)pairs, (unsigned)((p.a.K * p.a.V + NTH - 1) / NTH)), dim3(NTH), 0, s, p);
+  }
+  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, REV, OBF, false>), grid(p.items), dim3(NTH), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int KP, bool REV>
+hipError_t launch_types(const SweepPlan& p, hipStream_t s) {
+  if (!p.a.bf16) return launch<KP, false, 3, 3, REV, false>(p, s);
+  if (!p.a.out_bf16) return launch<KP, true, 3, 3, REV, false>(p, s);
+  return p.a.s_out ? launch<KP, true, 1, 3, REV, true>(p, s) : launch<KP, true, 1, 2, REV, true>(p, s);
+}
+
+}  // namespace
+
+}  // namespace linattn

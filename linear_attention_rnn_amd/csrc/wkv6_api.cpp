@@ -12,16 +12,14 @@
 #include <string>
 #include <vector>
 
+#include "wkv6_host.h"
 #include "wkv6_internal.h"
 
 namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int status, const std::string& msg) {
-  g_last_error = msg;
-  return status;
-}
+int fail(int status, const std::string& msg) { return wkv6::set_error(status, msg); }
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
@@ -112,12 +110,7 @@ hipError_t device_pool(hipMemPool_t* out, bool create) {
   return hipSuccess;
 }
 
-hipError_t ws_alloc(void** p, size_t bytes, hipStream_t s) {
-  hipMemPool_t pool = nullptr;
-  const hipError_t e = device_pool(&pool, true);
-  if (e != hipSuccess) return e;
-  return hipMallocFromPoolAsync(p, bytes, pool, s);
-}
+hipError_t ws_alloc(void** p, size_t bytes, hipStream_t s) { return wkv6::workspace_alloc(p, bytes, s); }
 
 // Workspace (stream-ordered) and kernels.
 int run(const wkv6::FwdArgs& a, hipStream_t s) {
@@ -159,6 +152,22 @@ wkv6::FwdArgs make_args(int64_t B, int64_t T, int64_t C, int64_t H, const void* 
 }
 
 }  // namespace
+
+namespace wkv6 {
+
+int set_error(int status, const std::string& msg) {
+  g_last_error = msg;
+  return status;
+}
+
+hipError_t workspace_alloc(void** p, size_t bytes, hipStream_t s) {
+  hipMemPool_t pool = nullptr;
+  const hipError_t e = device_pool(&pool, true);
+  if (e != hipSuccess) return e;
+  return hipMallocFromPoolAsync(p, bytes, pool, s);
+}
+
+}  // namespace wkv6
 
 extern "C" {
 

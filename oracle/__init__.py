@@ -18,7 +18,10 @@ Contents (all arithmetic in float64 on the exact input values):
 * ``wkv4_ref``         -- RWKV-4: the normalised per-channel (vector-state)
                           operator, in its recurrent form;
 * ``group_norm_heads``, ``wkv6_gn_ref`` -- the per-head group normalisation
-                          and gate that follow the operator in a block.
+                          and gate that follow the operator in a block;
+* ``linattn_oracle``   -- (imported as a module) attention with one decay per
+                          head and its gradients, rotary positions,
+                          root-mean-square norm, e4m3 rounding.
 
 Every function here is pinned by tests that do not rely on the oracle itself
 (closed forms, a hand-worked example, invariants, brute force on tiny inputs);

@@ -1,0 +1,33 @@
+// Host-only stand-ins for the kernel side of the linear-attention operators
+// (linattn_internal.h): they enqueue nothing and count the calls that got past
+// the argument checks.
+#include "linattn_internal.h"
+
+int g_linattn_enqueued = 0;
+
+namespace linattn {
+
+size_t sweep_workspace_bytes(const Sweep& a) { return a.T > 1000 ? (size_t)a.K * a.V * 4 : 0; }
+hipError_t enqueue_sweep(const Sweep&, void*, hipStream_t) {
+  ++g_linattn_enqueued;
+  return hipSuccess;
+}
+hipError_t enqueue_state_copy(const float*, float*, int64_t, hipStream_t) {
+  ++g_linattn_enqueued;
+  return hipSuccess;
+}
+hipError_t enqueue_rope(const Rope&, hipStream_t) {
+  ++g_linattn_enqueued;
+  return hipSuccess;
+}
+hipError_t enqueue_norm(const Norm&, hipStream_t) {
+  ++g_linattn_enqueued;
+  return hipSuccess;
+}
+size_t norm_bwd_workspace_bytes(const NormBwd&) { return 256; }
+hipError_t enqueue_norm_bwd(const NormBwd&, void*, hipStream_t) {
+  ++g_linattn_enqueued;
+  return hipSuccess;
+}
+
+}  // namespace linattn

@@ -1,0 +1,202 @@
+"""linattn.h against the built library on a host without a GPU: every declared
+function is exported, and every refusal of the documented calls comes back
+with its status and a text before anything is enqueued."""
+import ctypes
+import os
+import re
+
+import pytest
+
+from linear_attention_rnn_amd import linattn, wkv6
+
+pytestmark = pytest.mark.skipif(not os.path.exists(wkv6.LIB_PATH), reason="libwkv6.so not built")
+
+HEADER = os.path.join(os.path.dirname(wkv6.HEADER), "linattn.h")
+A = 0x100000000   # fake, aligned addresses far apart: never dereferenced by a refused call
+OK, INVALID, UNSUPPORTED, MISALIGNED = wkv6.OK, wkv6.ERR_INVALID_ARG, wkv6.ERR_UNSUPPORTED, wkv6.ERR_MISALIGNED
+
+
+def P(i):
+    return A * (i + 1)
+
+
+def test_exports_and_version():
+    with open(HEADER) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = set(re.findall(r"^\s*(?:int|size_t)\s+(linattn_\w+)\s*\(", text, flags=re.M))
+    assert names == {"linattn_fwd", "linattn_fwd_workspace_bytes", "linattn_bwd", "linattn_bwd_workspace_bytes",
+                     "linattn_rope", "linattn_rms_norm", "linattn_rms_norm_q8", "linattn_rms_norm_bwd",
+                     "linattn_rms_norm_bwd_workspace_bytes", "linattn_abi_version"}
+    for n in names:
+        assert ctypes.cast(getattr(linattn.lib(), n), ctypes.c_void_p).value
+    value = lambda m: int(re.search(rf"#define {m}\s+(\d+)", text).group(1))  # noqa: E731
+    assert linattn.abi_version() == value("LINATTN_ABI_VERSION") == 1
+    assert linattn.MAX_HEAD == value("LINATTN_MAX_HEAD")
+    assert linattn.MAX_COLUMNS == value("LINATTN_MAX_COLUMNS")
+
+
+def refused(status, want, text=""):
+    assert status == want, wkv6.last_error()
+    assert wkv6.last_error() and text in wkv6.last_error()
+
+
+# ---- linattn_fwd: pointers q k v log_decay lengths s_in o s_out
+def fwd(B=2, T=9, H=2, K=64, V=64, dtype=1, out=1, strides=None, ws=(0, 0), **p):
+    q = {n: P(i) for i, n in enumerate(("q", "k", "v", "log_decay", "lengths", "s_in", "o", "s_out"))}
+    q.update(p)
+    s = (ctypes.c_int64 * 12)(*strides) if strides else None
+    return linattn.lib().linattn_fwd(B, T, H, K, V, q["q"], q["k"], q["v"], q["log_decay"], 1.0, q["lengths"],
+                                     q["s_in"], q["o"], q["s_out"], s, dtype, out, *ws, 0)
+
+
+CONTIGUOUS = [9 * 128, 128, 64] * 4
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(dtype=2), INVALID),
+    (dict(out=7), INVALID), (dict(dtype=0, out=1), UNSUPPORTED), (dict(K=0), UNSUPPORTED), (dict(K=60), UNSUPPORTED),
+    (dict(V=136), UNSUPPORTED), (dict(K=256), UNSUPPORTED), (dict(B=2 ** 22, H=2), UNSUPPORTED),
+    (dict(B=2 ** 62, H=2 ** 20), UNSUPPORTED), (dict(T=2 ** 31), UNSUPPORTED),
+    (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID), (dict(log_decay=0), INVALID), (dict(o=0), INVALID),
+    (dict(q=P(0) + 4), MISALIGNED), (dict(lengths=P(4) + 4), MISALIGNED), (dict(s_in=P(5) + 8), MISALIGNED),
+    (dict(s_out=P(7) + 4), MISALIGNED), (dict(o=P(6) + 2), MISALIGNED),
+    (dict(o=P(0)), INVALID), (dict(o=P(2) + 64), INVALID), (dict(s_out=P(6)), INVALID), (dict(s_out=P(5) + 64), INVALID),
+    (dict(s_out=P(1)), INVALID), (dict(o=P(3) - 64), INVALID), (dict(o=P(4)), INVALID), (dict(o=P(5)), INVALID),
+    (dict(strides=[-128] + CONTIGUOUS[1:]), INVALID),
+    (dict(strides=CONTIGUOUS[:1] + [124] + CONTIGUOUS[2:]), MISALIGNED),
+    (dict(strides=CONTIGUOUS[:9] + [9 * 128, 128, 0]), INVALID),        # the output's heads in one place
+    (dict(strides=CONTIGUOUS[:9] + [9 * 128, 64, 64]), INVALID),        # its tokens overlap
+    (dict(strides=[2 ** 61] + CONTIGUOUS[1:]), UNSUPPORTED),
+    (dict(strides=[9 * 128, 2 ** 24, 64] + CONTIGUOUS[3:]), UNSUPPORTED),
+    (dict(B=1, H=1, T=4096, ws=(P(9), 16)), INVALID),                   # workspace too small
+    (dict(B=1, H=1, T=4096, ws=(P(9) + 4, 1 << 30)), MISALIGNED),
+])
+def test_fwd_refuses(kw, want):
+    refused(fwd(**kw), want)
+
+
+def test_fwd_without_work():
+    assert fwd(B=0, q=0, k=0, v=0, o=0, s_out=0) == OK
+    assert fwd(T=0, q=0, k=0, v=0, o=0, log_decay=0, s_out=0) == OK
+    refused(fwd(T=0, s_out=P(5) + 64), INVALID, "s_out overlaps s_in")
+
+
+def test_fwd_workspace_bytes():
+    bytes_ = linattn.fwd_workspace_bytes
+    assert bytes_(8, 4096, 32, 64, 64) == 0                  # 256 heads: no segments
+    assert bytes_(1, 8, 1, 64, 64) == 0 and bytes_(1, 64, 1, 64, 64) == 0
+    assert bytes_(-1, 64, 1, 64, 64) == 0 and bytes_(1, 64, 1, 63, 64) == 0
+    n = bytes_(1, 8192, 4, 128, 64)
+    assert n > 0 and n % (4 * 128 * 64 * 4) == 0 and 1 < n // (4 * 128 * 64 * 4) <= 128
+
+
+# ---- linattn_bwd
+BWD = ("q", "k", "v", "log_decay", "lengths", "s_in", "d_o", "ds_out", "dq", "dk", "dv", "ds_in")
+
+
+def bwd(B=2, T=9, H=2, K=64, V=64, dtype=1, grad=0, strides=None, ws=(0, 0), **p):
+    q = {n: P(i) for i, n in enumerate(BWD)}
+    q.update(p)
+    s = (ctypes.c_int64 * 21)(*strides) if strides else None
+    return linattn.lib().linattn_bwd(B, T, H, K, V, q["q"], q["k"], q["v"], q["log_decay"], 1.0, q["lengths"],
+                                     q["s_in"], q["d_o"], q["ds_out"], q["dq"], q["dk"], q["dv"], q["ds_in"], s, dtype,
+                                     grad, *ws, 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(H=0), INVALID), (dict(dtype=0, grad=1), UNSUPPORTED), (dict(K=12), UNSUPPORTED), (dict(V=256), UNSUPPORTED),
+    (dict(d_o=0), INVALID), (dict(dq=0), INVALID), (dict(dk=0), INVALID), (dict(dv=0), INVALID),
+    (dict(dv=P(10) + 4), MISALIGNED), (dict(ds_in=P(11) + 4), MISALIGNED),
+    (dict(dk=P(8)), INVALID), (dict(dv=P(2)), INVALID), (dict(ds_in=P(5)), INVALID), (dict(ds_in=P(7) + 64), INVALID),
+    (dict(dq=P(7)), INVALID), (dict(B=1, H=1, T=4096, ws=(P(20), 8)), INVALID),
+])
+def test_bwd_refuses(kw, want):
+    refused(bwd(**kw), want)
+
+
+def test_bwd_without_work():
+    assert bwd(B=0) == OK
+    assert bwd(T=0, ds_in=0) == OK
+
+
+# ---- linattn_rope
+def rope(B=2, T=3, H=2, D=64, R=64, layout=0, dtype=1, start=0, strides=None, **p):
+    q = {n: P(i) for i, n in enumerate(("q", "k", "q_out", "k_out", "positions", "freqs"))}
+    q.update(p)
+    s = (ctypes.c_int64 * 12)(*strides) if strides else None
+    return linattn.lib().linattn_rope(B, T, H, D, R, q["q"], q["k"], q["q_out"], q["k_out"], q["positions"], start,
+                                      q["freqs"], layout, 0, s, dtype, 0)
+
+
+ROWS = [3 * 128, 128, 64]
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), INVALID), (dict(H=0), INVALID), (dict(layout=2), INVALID), (dict(dtype=9), INVALID),
+    (dict(D=60), UNSUPPORTED), (dict(D=136), UNSUPPORTED), (dict(R=7), UNSUPPORTED), (dict(R=0), UNSUPPORTED),
+    (dict(R=66), UNSUPPORTED), (dict(B=2 ** 20, T=2 ** 20), UNSUPPORTED), (dict(start=2 ** 60), UNSUPPORTED),
+    (dict(q=0), INVALID), (dict(q_out=0), INVALID), (dict(k=0), INVALID), (dict(k_out=0), INVALID),
+    (dict(freqs=0), INVALID), (dict(freqs=P(5) + 8), MISALIGNED), (dict(q=P(0) + 8), MISALIGNED),
+    (dict(q_out=P(0) + 64), INVALID), (dict(q_out=P(1)), INVALID), (dict(k_out=P(2)), INVALID),
+    (dict(q_out=P(0), strides=ROWS + ROWS + [3 * 256, 256, 64] + ROWS), INVALID),   # in place, other distances
+    (dict(strides=ROWS + ROWS + [3 * 128, 128, 0] + ROWS), INVALID),
+])
+def test_rope_refuses(kw, want):
+    refused(rope(**kw), want)
+
+
+def test_rope_without_work():
+    assert rope(B=0) == OK and rope(T=0) == OK
+
+
+# ---- linattn_rms_norm, _q8, _bwd
+def norm(rows=4, C=256, eps=1e-5, dtype=1, **p):
+    q = {n: P(i) for i, n in enumerate(("x", "residual", "weight", "h", "y"))}
+    q.update(p)
+    return linattn.lib().linattn_rms_norm(rows, C, q["x"], q["residual"], q["weight"], eps, q["h"], q["y"], dtype, 0)
+
+
+def q8(rows=4, C=256, eps=1e-5, dtype=1, group=128, **p):
+    q = {n: P(i) for i, n in enumerate(("x", "residual", "weight", "h", "codes", "scales"))}
+    q.update(p)
+    return linattn.lib().linattn_rms_norm_q8(rows, C, q["x"], q["residual"], q["weight"], eps, q["h"], q["codes"],
+                                             q["scales"], group, dtype, 0)
+
+
+def norm_bwd(rows=4, C=256, eps=1e-5, dtype=1, ws=(0, 0), **p):
+    q = {n: P(i) for i, n in enumerate(("dy", "h", "dh", "weight", "dx", "dweight"))}
+    q.update(p)
+    return linattn.lib().linattn_rms_norm_bwd(rows, C, q["dy"], q["h"], q["dh"], q["weight"], eps, q["dx"],
+                                              q["dweight"], dtype, *ws, 0)
+
+
+SIZES = [(dict(rows=-1), INVALID), (dict(C=0), INVALID), (dict(C=100), UNSUPPORTED), (dict(C=16392), UNSUPPORTED),
+         (dict(rows=2 ** 23), UNSUPPORTED), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+         (dict(eps=float("inf")), INVALID), (dict(dtype=4), INVALID)]
+
+
+@pytest.mark.parametrize("kw,want", SIZES + [
+    (dict(x=0), INVALID), (dict(weight=0), INVALID), (dict(y=0), INVALID), (dict(h=0), INVALID),
+    (dict(residual=0), INVALID), (dict(x=P(0) + 2), MISALIGNED), (dict(y=P(0)), INVALID), (dict(y=P(3)), INVALID),
+    (dict(h=P(0) + 512), INVALID), (dict(h=P(2)), INVALID)])
+def test_norm_refuses(kw, want):
+    refused(norm(**kw), want)
+
+
+@pytest.mark.parametrize("kw,want", SIZES + [
+    (dict(group=64), INVALID), (dict(codes=0), INVALID), (dict(scales=0), INVALID), (dict(scales=P(5) + 4), MISALIGNED),
+    (dict(codes=P(0)), INVALID), (dict(scales=P(4)), INVALID)])
+def test_q8_refuses(kw, want):
+    refused(q8(**kw), want)
+
+
+@pytest.mark.parametrize("kw,want", SIZES + [
+    (dict(dy=0), INVALID), (dict(h=0), INVALID), (dict(dx=0), INVALID), (dict(dweight=0), INVALID),
+    (dict(dx=P(1)), INVALID), (dict(dx=P(0) + 512), INVALID), (dict(dweight=P(3)), INVALID), (dict(dweight=P(4)), INVALID),
+    (dict(ws=(P(9), 4)), INVALID), (dict(ws=(P(9) + 4, 1 << 30)), MISALIGNED)])
+def test_norm_bwd_refuses(kw, want):
+    refused(norm_bwd(**kw), want)
+
+
+def test_norm_without_rows():
+    assert norm(rows=0) == OK and q8(rows=0) == OK
