@@ -77,6 +77,9 @@ def bwd_workspace_bytes(B, T, H, K, V, dtype=torch.bfloat16, grad_dtype=torch.fl
 
 
 # ---------------------------------------------------------------- checks
+# These run before every call and are most of what a call costs the host next
+# to the launch itself (3.5 us of 7 for a single-token step), hence few and
+# plain expressions.
 def _dtype(t, name):
     d = _DTYPES.get(t.dtype)
     if d is None:
@@ -85,20 +88,23 @@ def _dtype(t, name):
 
 
 def _tensor(t, name, shape, dtype, device):
-    """A [B, T, H, D] tensor with adjacent channels on the call's GPU."""
-    if t.shape != shape or t.dtype != dtype:
+    """A [B, T, H, D] tensor with adjacent channels on the call's GPU; returns
+    its address."""
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the GPU of the first tensor")
-    if shape[3] > 1 and not t.is_contiguous() and t.stride(3) != 1:
+    if t.device != device:
+        raise ValueError(f"{name} must be on the GPU of the first tensor, {device}")
+    if not t.is_contiguous() and t.stride(3) != 1 and shape[3] > 1:
         raise ValueError(f"the channels of {name} must be adjacent")
+    return t.data_ptr()
 
 
 def _flat(t, name, shape, dtype, device):
-    """A contiguous tensor of one shape and type on the call's GPU, or None."""
+    """A contiguous tensor of one shape and type on the call's GPU; returns its
+    address, 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
     return t.data_ptr()
 
@@ -116,21 +122,23 @@ def _strides(*tensors):
     return (ctypes.c_int64 * len(out))(*out)
 
 
-class _On:
-    """Makes the inputs' GPU current for the call if it is not."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    __slots__ = ("guard",)
 
-    def __init__(self, device):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _call(name, f, device, stream, *args):
+    """The library call, with the inputs' GPU current and on `stream` or torch's
+    current one."""
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = _stream_handle(stream, device)
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, handle)
+    if status != OK:
+        raise LinattnError(name, status)
 
 
 def _workspace(given, need, device, stream):
@@ -138,7 +146,7 @@ def _workspace(given, need, device, stream):
     its bytes.  Nothing, unless it was given or the current stream records a
     graph: then the library's pool serves."""
     if given is not None:
-        if given.dtype != torch.uint8 or not given.is_cuda or given.device != device or not given.is_contiguous():
+        if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
         return given.data_ptr(), given.numel(), given
     if stream is None and torch.cuda.is_current_stream_capturing():
@@ -149,22 +157,18 @@ def _workspace(given, need, device, stream):
     return 0, 0, None
 
 
-def _raise(name, status):
-    if status != OK:
-        raise LinattnError(name, status)
-
-
 def _attention(q, k, v, log_decay, lengths):
+    """Sizes, type, GPU and addresses of what fwd and bwd have in common."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be [B, T, H, channels]")
-    B, T, H, K = q.shape
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    shape, t, dev = q.shape, q.dtype, q.device
+    B, T, H, K = shape
     V = v.shape[3]
     dtype = _dtype(q, "q, k, v")
-    dev = q.device
-    _tensor(q, "q", q.shape, q.dtype, dev)
-    _tensor(k, "k", q.shape, q.dtype, dev)
-    _tensor(v, "v", (B, T, H, V), q.dtype, dev)
-    return (B, T, H, K, V, dtype, dev, _flat(log_decay, "log_decay", (H,), torch.float32, dev),
+    return (B, T, H, K, V, dtype, dev, _tensor(q, "q", shape, t, dev), _tensor(k, "k", shape, t, dev),
+            _tensor(v, "v", (B, T, H, V), t, dev), _flat(log_decay, "log_decay", (H,), torch.float32, dev),
             _flat(lengths, "lengths", (B,), torch.int32, dev))
 
 
@@ -186,24 +190,22 @@ def fwd(q, k, v, log_decay, scale: float = 1.0, lengths=None, s_in=None, want_st
     s_in), or to a new tensor if `want_state`; otherwise None is returned for
     it.
     """
-    B, T, H, K, V, dtype, dev, pg, pl = _attention(q, k, v, log_decay, lengths)
+    B, T, H, K, V, dtype, dev, pq, pk, pv, pg, pl = _attention(q, k, v, log_decay, lengths)
     if out is None:
         out = torch.empty((B, T, H, V), dtype=out_dtype or q.dtype, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out must have out_dtype")
     odt = _dtype(out, "out")
-    _tensor(out, "out", (B, T, H, V), out.dtype, dev)
+    py = _tensor(out, "out", (B, T, H, V), out.dtype, dev)
     ps = _flat(s_in, "s_in", (B, H, K, V), torch.float32, dev)
     if s_out is None and want_state:
         s_out = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
     po = _flat(s_out, "s_out", (B, H, K, V), torch.float32, dev)
     L = lib()
-    with _On(dev):
-        pw, nw, keep = _workspace(
-            workspace, lambda: L.linattn_fwd_workspace_bytes(B, T, H, K, V, dtype, odt, po != 0), dev, stream)
-        _raise("linattn_fwd", L.linattn_fwd(
-            B, T, H, K, V, q.data_ptr(), k.data_ptr(), v.data_ptr(), pg, scale, pl, ps, out.data_ptr(), po,
-            _strides(q, k, v, out), dtype, odt, pw, nw, _stream_handle(stream, dev)))
+    pw, nw, keep = _workspace(
+        workspace, lambda: L.linattn_fwd_workspace_bytes(B, T, H, K, V, dtype, odt, po != 0), dev, stream)
+    _call("linattn_fwd", L.linattn_fwd, dev, stream, B, T, H, K, V, pq, pk, pv, pg, scale, pl, ps, py, po,
+          _strides(q, k, v, out), dtype, odt, pw, nw)
     return out, s_out
 
 
@@ -218,8 +220,8 @@ def bwd(q, k, v, log_decay, do, scale: float = 1.0, lengths=None, s_in=None, ds_
     are fine).  Expanded inputs get the gradient of every place they are used
     at: the caller sums them.
     """
-    B, T, H, K, V, dtype, dev, pg, pl = _attention(q, k, v, log_decay, lengths)
-    _tensor(do, "do", (B, T, H, V), q.dtype, dev)
+    B, T, H, K, V, dtype, dev, pq, pk, pv, pg, pl = _attention(q, k, v, log_decay, lengths)
+    pdo = _tensor(do, "do", (B, T, H, V), q.dtype, dev)
     ps = _flat(s_in, "s_in", (B, H, K, V), torch.float32, dev)
     pd = _flat(ds_out, "ds_out", (B, H, K, V), torch.float32, dev)
     g = dict(out) if out else {}
@@ -232,13 +234,11 @@ def bwd(q, k, v, log_decay, do, scale: float = 1.0, lengths=None, s_in=None, ds_
         g["s_in"] = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
     pi = _flat(g.get("s_in"), "ds_in", (B, H, K, V), torch.float32, dev)
     L = lib()
-    with _On(dev):
-        pw, nw, keep = _workspace(
-            workspace, lambda: L.linattn_bwd_workspace_bytes(B, T, H, K, V, dtype, gdt, pi != 0), dev, stream)
-        _raise("linattn_bwd", L.linattn_bwd(
-            B, T, H, K, V, q.data_ptr(), k.data_ptr(), v.data_ptr(), pg, scale, pl, ps, do.data_ptr(), pd,
-            g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(), pi,
-            _strides(q, k, v, do, g["q"], g["k"], g["v"]), dtype, gdt, pw, nw, _stream_handle(stream, dev)))
+    pw, nw, keep = _workspace(
+        workspace, lambda: L.linattn_bwd_workspace_bytes(B, T, H, K, V, dtype, gdt, pi != 0), dev, stream)
+    _call("linattn_bwd", L.linattn_bwd, dev, stream, B, T, H, K, V, pq, pk, pv, pg, scale, pl, ps, pdo, pd,
+          g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(), pi,
+          _strides(q, k, v, do, g["q"], g["k"], g["v"]), dtype, gdt, pw, nw)
     return g
 
 
@@ -291,29 +291,29 @@ def rope(q, k, freqs, positions=None, start: int = 0, layout: str = "half", inve
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, D]")
-    B, T, H, D = q.shape
-    dtype, dev = _dtype(q, "q and k"), q.device
-    _tensor(q, "q", q.shape, q.dtype, dev)
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    shape, t, dev = q.shape, q.dtype, q.device
+    B, T, H, D = shape
+    dtype = _dtype(q, "q and k")
+    pq = _tensor(q, "q", shape, t, dev)
     if freqs is None or freqs.dim() != 1:
         raise ValueError("freqs must be a float64 vector of R / 2 values")
     pf = _flat(freqs, "freqs", freqs.shape, torch.float64, dev)
     pp = _flat(positions, "positions", (B, T), torch.int32, dev)
     if q_out is None:
-        q_out = torch.empty((B, T, H, D), dtype=q.dtype, device=dev)
-    _tensor(q_out, "q_out", q.shape, q.dtype, dev)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    pqo = _tensor(q_out, "q_out", shape, t, dev)
     pk = pko = 0
     if k is not None:
-        _tensor(k, "k", q.shape, q.dtype, dev)
+        pk = _tensor(k, "k", shape, t, dev)
         if k_out is None:
-            k_out = torch.empty((B, T, H, D), dtype=q.dtype, device=dev)
-        _tensor(k_out, "k_out", q.shape, q.dtype, dev)
-        pk, pko = k.data_ptr(), k_out.data_ptr()
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        pko = _tensor(k_out, "k_out", shape, t, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    with _On(dev):
-        _raise("linattn_rope", lib().linattn_rope(
-            B, T, H, D, 2 * freqs.shape[0], q.data_ptr(), pk, q_out.data_ptr(), pko, pp, start, pf,
-            _LAYOUTS[layout], inverse, _strides(q, k, q_out, k_out), dtype, _stream_handle(stream, dev)))
+    _call("linattn_rope", lib().linattn_rope, dev, stream, B, T, H, D, 2 * freqs.shape[0], pq, pk, pqo, pko, pp, start,
+          pf, _LAYOUTS[layout], inverse, _strides(q, k, q_out, k_out), dtype)
     return q_out, k_out
 
 
@@ -342,7 +342,7 @@ def _rows(x, weight):
     if x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous GPU tensor [..., C]")
     C = x.shape[-1]
-    rows = x.numel() // C if C else 0
+    rows = x.shape[0] if x.dim() == 2 else x.numel() // C if C else 0
     return rows, C, _dtype(x, "x"), x.device, _flat(weight, "weight", (C,), torch.float32, x.device)
 
 
@@ -368,9 +368,7 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, h=None, out=None, stre
     if out is None:
         out = torch.empty_like(x)
     py = _flat(out, "out", x.shape, x.dtype, dev)
-    with _On(dev):
-        _raise("linattn_rms_norm", lib().linattn_rms_norm(rows, C, x.data_ptr(), pr, pw, eps, ph, py, dtype,
-                                                          _stream_handle(stream, dev)))
+    _call("linattn_rms_norm", lib().linattn_rms_norm, dev, stream, rows, C, x.data_ptr(), pr, pw, eps, ph, py, dtype)
     return out, h
 
 
@@ -384,15 +382,14 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, group: int = 128, h
         raise ValueError("group must be 0 or 128")
     h, pr, ph = _residual(x, residual, h)
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     pc = _flat(codes, "codes", x.shape, torch.float8_e4m3fn, dev)
     shape = (*x.shape[:-1], (C + 127) // 128 if group else 1)
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=dev)
     ps = _flat(scales, "scales", shape, torch.float32, dev)
-    with _On(dev):
-        _raise("linattn_rms_norm_q8", lib().linattn_rms_norm_q8(rows, C, x.data_ptr(), pr, pw, eps, ph, pc, ps, group,
-                                                                dtype, _stream_handle(stream, dev)))
+    _call("linattn_rms_norm_q8", lib().linattn_rms_norm_q8, dev, stream, rows, C, x.data_ptr(), pr, pw, eps, ph, pc, ps,
+          group, dtype)
     return codes, scales, h
 
 
@@ -410,9 +407,7 @@ def rms_norm_bwd(dy, h, weight, eps: float = 1e-6, dh=None, out=None, workspace=
     px = _flat(out, "out", h.shape, h.dtype, dev)
     dweight = torch.empty((C,), dtype=torch.float32, device=dev)
     L = lib()
-    with _On(dev):
-        pws, nws, keep = _workspace(workspace, lambda: L.linattn_rms_norm_bwd_workspace_bytes(rows, C, dtype), dev, stream)
-        _raise("linattn_rms_norm_bwd", L.linattn_rms_norm_bwd(
-            rows, C, pdy, h.data_ptr(), pdh, pw, eps, px, dweight.data_ptr(), dtype, pws, nws,
-            _stream_handle(stream, dev)))
+    pws, nws, keep = _workspace(workspace, lambda: L.linattn_rms_norm_bwd_workspace_bytes(rows, C, dtype), dev, stream)
+    _call("linattn_rms_norm_bwd", L.linattn_rms_norm_bwd, dev, stream, rows, C, pdy, h.data_ptr(), pdh, pw, eps, px,
+          dweight.data_ptr(), dtype, pws, nws)
     return {"x": out, "weight": dweight}
