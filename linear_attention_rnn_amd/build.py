@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libwkv6.so")
 SOURCES = ["wkv6_kernels.hip", "wkv6_backward.hip", "wkv6_backward_chunked.hip", "wkv4_kernels.hip", "wkv6_groupnorm.hip", "wkv6_api.cpp",
-           "linattn_forward.hip", "linattn_reverse.hip", "linattn_rope.hip", "linattn_norm.hip", "linattn_api.cpp"]
+           "linattn_plan.hip", "linattn_sweep64.hip", "linattn_sweep128.hip", "linattn_rope.hip", "linattn_norm.hip", "linattn_api.cpp"]
 ARCH = "gfx950"
 
 

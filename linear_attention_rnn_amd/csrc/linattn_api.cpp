@@ -284,7 +284,7 @@ size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
   linattn::Sweep a = base_sweep(B, T, H, K, V, nullptr, nullptr, dtype, out_dtype);
   float any = 0.f;
   a.s_out = state_out ? &any : nullptr;
-  return linattn::sweep_workspace_bytes(a);
+  return linattn::sweep_workspace_bytes(&a, 1);
 }
 
 int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const void* q, const void* k, const void* v,
@@ -321,8 +321,8 @@ int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   a.s_in = s_in;
   a.s_out = s_out;
   Workspace ws(hs);
-  if ((st = ws.take(workspace, workspace_bytes, linattn::sweep_workspace_bytes(a))) != WKV6_OK) return st;
-  return ws.done(linattn::enqueue_sweep(a, ws.p, hs));
+  if ((st = ws.take(workspace, workspace_bytes, linattn::sweep_workspace_bytes(&a, 1))) != WKV6_OK) return st;
+  return ws.done(linattn::enqueue_sweeps(&a, 1, ws.p, hs));
 }
 
 size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, int dtype, int grad_dtype,
@@ -333,9 +333,7 @@ size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
   linattn::Sweep w[3];
   float any = 0.f;
   bwd_sweeps(B, T, H, K, V, nullptr, 1.f, nullptr, nullptr, nullptr, state_grad ? &any : nullptr, none, dtype, grad_dtype, w);
-  size_t most = 0;   // the sweeps run one after another and share it
-  for (const linattn::Sweep& x : w) most = std::max(most, linattn::sweep_workspace_bytes(x));
-  return most;
+  return linattn::sweep_workspace_bytes(w, 3);
 }
 
 int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const void* q, const void* k, const void* v,
@@ -375,14 +373,9 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   if (T == 0) return finished(linattn::enqueue_state_copy(ds_out, ds_in, B * H * K * V, hs));
   linattn::Sweep w[3];
   bwd_sweeps(B, T, H, K, V, log_decay, scale, lengths, s_in, ds_out, ds_in, t, dtype, grad_dtype, w);
-  size_t most = 0;
-  for (const linattn::Sweep& x : w) most = std::max(most, linattn::sweep_workspace_bytes(x));
   Workspace ws(hs);
-  if ((st = ws.take(workspace, workspace_bytes, most)) != WKV6_OK) return st;
-  hipError_t e = hipSuccess;
-  for (const linattn::Sweep& x : w)
-    if (e == hipSuccess) e = linattn::enqueue_sweep(x, ws.p, hs);
-  return ws.done(e);
+  if ((st = ws.take(workspace, workspace_bytes, linattn::sweep_workspace_bytes(w, 3))) != WKV6_OK) return st;
+  return ws.done(linattn::enqueue_sweeps(w, 3, ws.p, hs));
 }
 
 int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const void* q, const void* k, void* q_out,

@@ -45,21 +45,28 @@ struct Sweep {
   bool out_bf16;
 };
 
-size_t sweep_workspace_bytes(const Sweep& a);
-// `workspace`: sweep_workspace_bytes(a) bytes, or null where that is 0.
-hipError_t enqueue_sweep(const Sweep& a, void* workspace, hipStream_t stream);
+// Up to three sweeps over the same sequences, types and product K V, run side
+// by side: none reads what another writes, except that the last one's s_out
+// may be another one's s_in.
+constexpr int kSweeps = 3;
+size_t sweep_workspace_bytes(const Sweep* a, int n);
+// `workspace`: sweep_workspace_bytes bytes, or null where that is 0.
+hipError_t enqueue_sweeps(const Sweep* a, int n, void* workspace, hipStream_t stream);
 
-// How a sweep is laid over the card.
+// How sweeps are laid over the card.
 struct SweepPlan {
-  Sweep a;
-  float* ws;        // [B H][segments] entering states, [K][V]; null for one segment
+  Sweep a[kSweeps];
+  int sweeps;
+  bool state_out;   // the call hands back a state
+  float* ws;        // [sweeps][B H][segments] entering states, [K][V]; null for one segment
   int segments;     // of each sequence
   int seg_tokens;   // tokens of a segment, a multiple of 64
-  int vblocks;      // blocks of 64 value channels
-  int64_t items;    // workgroups / vblocks
+  int vblocks;      // blocks of 64 value channels, the most of the sweeps
+  int64_t pairs;    // B H
+  int64_t items;    // pairs * segments
 };
-hipError_t launch_forward(const SweepPlan& p, hipStream_t s);
-hipError_t launch_reverse(const SweepPlan& p, hipStream_t s);
+hipError_t launch_sweeps64(const SweepPlan& p, hipStream_t s);    // K <= 64 in all sweeps
+hipError_t launch_sweeps128(const SweepPlan& p, hipStream_t s);
 
 // n floats from `from` (zeros where it is null) to `to`; n is a multiple of 4.
 hipError_t enqueue_state_copy(const float* from, float* to, int64_t n, hipStream_t stream);

@@ -1,5 +1,7 @@
-// Linear attention with one decay for each head: the forward sweeps, the
-// token-by-token steps and the plan of a call.
+// Linear attention with one decay for each head: the token-by-token steps and
+// the plan of a call.
+#include <algorithm>
+
 #include "linattn_sweep.h"
 
 namespace linattn {
@@ -109,31 +111,30 @@ hipError_t launch_steps(const Sweep& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool steps(const Sweep& a) { return a.T <= kStepTokens && !a.reverse && !a.s_transposed; }
+bool steps(const Sweep* a, int n) { return n == 1 && a->T <= kStepTokens && !a->reverse && !a->s_transposed; }
 
-SweepPlan plan(const Sweep& a) {
-  SweepPlan p;
-  p.a = a;
-  p.ws = nullptr;
-  p.vblocks = (a.V + kVBlock - 1) / kVBlock;
-  const int64_t chunks = (a.T + kChunk - 1) / kChunk, groups = a.B * a.H * p.vblocks;
-  // Two workgroups for each of the 256 CUs; segments of at least four chunks.
+SweepPlan plan(const Sweep* a, int n) {
+  SweepPlan p = {};
+  p.sweeps = n;
+  p.vblocks = 1;
+  for (int i = 0; i < n; ++i) {
+    p.a[i] = a[i];
+    p.state_out = p.state_out || a[i].s_out;
+    p.vblocks = std::max(p.vblocks, (a[i].V + kVBlock - 1) / kVBlock);
+  }
+  p.pairs = a->B * a->H;
+  const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * p.vblocks * n;
+  // Two workgroups for each of the 256 CUs; segments of at least two chunks.
   int64_t G = groups >= 256 ? 1 : (512 + groups - 1) / groups;
-  if (G > chunks / 4) G = chunks / 4;
-  if (G < 1) G = 1;
+  G = std::max<int64_t>(1, std::min(G, chunks / 2));
   const int64_t per = (chunks + G - 1) / G;
   p.seg_tokens = (int)(per * kChunk);
   p.segments = (int)((chunks + per - 1) / per);
-  if (p.segments < 1) p.segments = 1;
-  p.items = a.B * a.H * p.segments;
+  p.items = p.pairs * p.segments;
   return p;
 }
 
 }  // namespace
-
-hipError_t launch_forward(const SweepPlan& p, hipStream_t s) {
-  return p.a.K <= 64 ? launch_types<64, false>(p, s) : launch_types<128, false>(p, s);
-}
 
 hipError_t enqueue_state_copy(const float* from, float* to, int64_t n, hipStream_t s) {
   if (from == to || n == 0) return hipSuccess;
@@ -143,18 +144,31 @@ hipError_t enqueue_state_copy(const float* from, float* to, int64_t n, hipStream
   return hipGetLastError();
 }
 
-size_t sweep_workspace_bytes(const Sweep& a) {
-  if (steps(a)) return 0;
-  const SweepPlan p = plan(a);
+size_t sweep_workspace_bytes(const Sweep* a, int n) {
+  if (steps(a, n)) return 0;
+  const SweepPlan p = plan(a, n);
   if (p.segments == 1) return 0;
-  return ((size_t)p.items * a.K * a.V * 4 + 255) / 256 * 256;
+  return ((size_t)n * p.items * a->K * a->V * 4 + 255) / 256 * 256;
 }
 
-hipError_t enqueue_sweep(const Sweep& a, void* workspace, hipStream_t s) {
-  if (steps(a)) return a.K <= 64 ? launch_steps<4>(a, s) : launch_steps<8>(a, s);
-  SweepPlan p = plan(a);
+hipError_t enqueue_sweeps(const Sweep* a, int n, void* workspace, hipStream_t s) {
+  if (steps(a, n)) return a->K <= 64 ? launch_steps<4>(*a, s) : launch_steps<8>(*a, s);
+  SweepPlan p = plan(a, n);
   if (p.segments > 1) p.ws = static_cast<float*>(workspace);
-  return a.reverse ? launch_reverse(p, s) : launch_forward(p, s);
+  int K = 0;
+  for (int i = 0; i < n; ++i) K = std::max(K, a[i].K);
+  const auto launch = K <= 64 ? launch_sweeps64 : launch_sweeps128;
+  // A sweep that leaves its state where another one takes its own from goes
+  // last, after it (with segments, all states are read before the sweeps).
+  bool after = false;
+  for (int i = 0; i + 1 < n; ++i) after = after || (a[n - 1].s_out && a[n - 1].s_out == a[i].s_in);
+  if (!after || p.segments > 1) return launch(p, s);
+  p.sweeps = n - 1;
+  const hipError_t e = launch(p, s);
+  if (e != hipSuccess) return e;
+  p.sweeps = 1;
+  p.a[0] = a[n - 1];
+  return launch(p, s);
 }
 
 }  // namespace linattn

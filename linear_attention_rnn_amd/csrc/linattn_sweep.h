@@ -1,7 +1,6 @@
 // Linear attention with one decay for each head: the chunked sweep on matrix
-// cores and its segment carries.  Included by the two files that instantiate
-// it (linattn_forward.hip,
-// linattn_reverse.hip).
+// cores and its segment carries.  Included by the files that instantiate
+// it (linattn_sweep64.hip, linattn_sweep128.hip).
 //
 // Mathematics, for a chunk of n <= 64 tokens in sweep order with the state M
 // (K x V) entering it, a the decay, d = 0 for the forward sweep and 1 for the
@@ -124,8 +123,13 @@ __device__ __forceinline__ Op<S> read_tr(const __bf16* p, int stride, int o0, in
   return o;
 }
 
-template <int KP, bool BF, int MP, int UP, bool REV, bool OBF, bool SUMMARY>
-__global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
+template <int KP, bool BF, int MP>
+constexpr int occupancy() {
+  return KP == 64 ? (BF && MP == 1 ? 3 : 2) : (BF ? 2 : 1);
+}
+
+template <int KP, bool BF, int MP, int UP, bool OBF, bool SUMMARY>
+__global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
   constexpr int NI = BF ? 1 : 3;             // parts of an input operand
   constexpr int ISZ = BF ? 2 : 4;
   constexpr int NJ = KP / 32;                // groups of 32 key channels
@@ -135,7 +139,8 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
   __shared__ __bf16 Vp[NI * kPlane];
   __shared__ __bf16 Sp[SUMMARY ? 8 : MP * KP * 64];
 
-  const Sweep& a = p.a;
+  const Sweep& a = p.a[blockIdx.y];
+  const bool rev = a.reverse;
   // Blocks of one item are 8 apart, so that they run on one XCD and share its L2.
   const int64_t item = (int64_t)(blockIdx.x / (8 * p.vblocks)) * 8 + blockIdx.x % 8;
   const int vb = (blockIdx.x / 8) % p.vblocks;
@@ -145,6 +150,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
   const int seg = (int)(item % segs);
   const int64_t b = pair / a.H, h = pair % a.H;
   const int v0 = vb * kVBlock;
+  if (v0 >= a.V) return;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const float gl = log2_decay(a.log_decay[h]);
@@ -161,7 +167,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
   int64_t cs = a.V, ns = 1;
   if constexpr (!SUMMARY) {
     if (p.ws)
-      s_from = p.ws + (pair * p.segments + seg) * a.K * a.V;
+      s_from = p.ws + ((blockIdx.y * p.pairs + pair) * p.segments + seg) * a.K * a.V;
     else if (a.s_in) {
       s_from = a.s_in + pair * a.K * a.V;
       if (a.s_transposed) cs = 1, ns = a.K;
@@ -178,7 +184,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
       }
 
   // ---- factors of whole chunks
-  const float f_inter = ex2(gl * (16 * w + li + (REV ? 0 : 1))) * a.is;   // column t = 16w + li
+  const float f_inter = ex2(gl * (16 * w + li + (rev ? 0 : 1))) * a.is;   // column t = 16w + li
   float dg[4], of[4];   // tile of the wave's own tokens; the tile before it
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -193,7 +199,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int d = nt - 1 + (REV ? 1 : 0) - (32 * u + 8 * g + j);
+        const int d = nt - 1 + (rev ? 1 : 0) - (32 * u + 8 * g + j);
         uf[u][j] = d >= 0 ? ex2(gl * d) * a.us : 0.f;
       }
   };
@@ -204,10 +210,10 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
   const auto load = [&](int c) {
     const int64_t at = lo + (int64_t)c * kChunk;
     const int nt = (int)(hi - at < kChunk ? hi - at : kChunk);
-    const int64_t a0 = REV ? len - at - nt : at;
+    const int64_t a0 = rev ? len - at - nt : at;
     const Rsrc rk = chunk_rsrc(a.k, b, h, a0, nt, a.K, ISZ), rv = chunk_rsrc(a.v, b, h, a0, nt, a.V, ISZ);
     const auto off = [&](int j, int64_t stride, int col, int D) {
-      return j < nt && col < D ? (REV ? nt - 1 - j : j) * (int)stride * ISZ + col * ISZ : wkv6::kOffNone;
+      return j < nt && col < D ? (rev ? nt - 1 - j : j) * (int)stride * ISZ + col * ISZ : wkv6::kOffNone;
     };
 #pragma unroll
     for (int x = 0; x < KR; ++x) {
@@ -231,7 +237,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
   for (int c = 0; c < nch; ++c) {
     const int64_t at = lo + (int64_t)c * kChunk;
     const int nt = (int)(hi - at < kChunk ? hi - at : kChunk);
-    const int64_t a0 = REV ? len - at - nt : at;
+    const int64_t a0 = rev ? len - at - nt : at;
     // ---- keys, values and the state to LDS
 #pragma unroll
     for (int x = 0; x < KR; ++x) {
@@ -306,7 +312,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
         const int j = 16 * w + li;
         constexpr int OSZ = OBF ? 2 : 4;
         const Rsrc ro = chunk_rsrc(a.o, b, h, a0, nt, a.V, OSZ);
-        const int orow = (REV ? nt - 1 - j : j) * (int)a.o.t;
+        const int orow = (rev ? nt - 1 - j : j) * (int)a.o.t;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int n = v0 + 32 * u + 8 * g;
@@ -368,7 +374,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
   // ---- hand on the state
   float* s_to = nullptr;
   if constexpr (SUMMARY)
-    s_to = p.ws + (pair * p.segments + seg) * a.K * a.V;
+    s_to = p.ws + ((blockIdx.y * p.pairs + pair) * p.segments + seg) * a.K * a.V;
   else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
     s_to = a.s_out + pair * a.K * a.V;
     cs = a.s_transposed ? 1 : a.V;
@@ -403,7 +409,7 @@ __global__ __launch_bounds__(NTH) void sweep_kernel(SweepPlan p) {
 // The segments' own states, as the summaries left them, become the states
 // that enter the segments: M_0 = s_in, M_{s+1} = a^(tokens of s) M_s + U_s.
 __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
-  const Sweep& a = p.a;
+  const Sweep& a = p.a[blockIdx.z];
   const int64_t pair = blockIdx.x;
   const int e = blockIdx.y * NTH + threadIdx.x, KV = a.K * a.V;
   if (e >= KV) return;
@@ -411,7 +417,7 @@ __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
   const float gl = log2_decay(a.log_decay[pair % a.H]);
   const int from = a.s_transposed ? (e % a.V) * a.K + e / a.V : e;
   float m = a.s_in ? a.s_in[pair * KV + from] : 0.f;
-  float* at = p.ws + pair * p.segments * KV + e;
+  float* at = p.ws + (blockIdx.z * p.pairs + pair) * p.segments * KV + e;
   for (int s = 0; s < p.segments; ++s, at += KV) {
     const float u = s + 1 < p.segments ? *at : 0.f;
     *at = m;
@@ -421,25 +427,25 @@ __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
   }
 }
 
-template <int KP, bool BF, int MP, int UP, bool REV, bool OBF>
-hipError_t launch(SweepPlan p, hipStream_t s) {
-  const int64_t pairs = p.a.B * p.a.H;
-  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.vblocks)); };
+template <int KP, bool BF, int MP, int UP, bool OBF>
+hipError_t launch(const SweepPlan& p, hipStream_t s) {
+  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.vblocks), p.sweeps); };
   if (p.segments > 1) {
     SweepPlan q = p;
-    q.items = pairs * (p.segments - 1);
-    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, REV, OBF, true>), grid(q.items), dim3(NTH), 0, s, q);
-    hipLaunchKernelGGL(carry_kernel, dim3((unsigned)pairs, (unsigned)((p.a.K * p.a.V + NTH - 1) / NTH)), dim3(NTH), 0, s, p);
+    q.items = p.pairs * (p.segments - 1);
+    const unsigned parts = (unsigned)((p.a[0].K * p.a[0].V + NTH - 1) / NTH);
+    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, true>), grid(q.items), dim3(NTH), 0, s, q);
+    hipLaunchKernelGGL(carry_kernel, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(NTH), 0, s, p);
   }
-  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, REV, OBF, false>), grid(p.items), dim3(NTH), 0, s, p);
+  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, false>), grid(p.items), dim3(NTH), 0, s, p);
   return hipGetLastError();
 }
 
-template <int KP, bool REV>
+template <int KP>
 hipError_t launch_types(const SweepPlan& p, hipStream_t s) {
-  if (!p.a.bf16) return launch<KP, false, 3, 3, REV, false>(p, s);
-  if (!p.a.out_bf16) return launch<KP, true, 3, 3, REV, false>(p, s);
-  return p.a.s_out ? launch<KP, true, 1, 3, REV, true>(p, s) : launch<KP, true, 1, 2, REV, true>(p, s);
+  if (!p.a[0].bf16) return launch<KP, false, 3, 3, false>(p, s);
+  if (!p.a[0].out_bf16) return launch<KP, true, 3, 3, false>(p, s);
+  return p.state_out ? launch<KP, true, 1, 3, true>(p, s) : launch<KP, true, 1, 2, true>(p, s);
 }
 
 }  // namespace

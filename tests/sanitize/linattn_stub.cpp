@@ -7,8 +7,8 @@ int g_linattn_enqueued = 0;
 
 namespace linattn {
 
-size_t sweep_workspace_bytes(const Sweep& a) { return a.T > 1000 ? (size_t)a.K * a.V * 4 : 0; }
-hipError_t enqueue_sweep(const Sweep&, void*, hipStream_t) {
+size_t sweep_workspace_bytes(const Sweep* a, int) { return a->T > 1000 ? (size_t)a->K * a->V * 4 : 0; }
+hipError_t enqueue_sweeps(const Sweep*, int, void*, hipStream_t) {
   ++g_linattn_enqueued;
   return hipSuccess;
 }
