@@ -10,8 +10,8 @@
 namespace linattn {
 
 constexpr int kChunk = 64;       // tokens of a chunk
-constexpr int kVBlock = 64;      // value channels one workgroup handles
 constexpr int kStepTokens = 8;   // calls of at most so many tokens run token by token
+constexpr int kVBlock = 64;      // value channels one workgroup handles
 
 // A [B, T, H, D] tensor: base and distances in elements (channels adjacent).
 struct Tensor {

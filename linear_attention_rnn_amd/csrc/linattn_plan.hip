@@ -7,6 +7,7 @@
 namespace linattn {
 namespace {
 
+
 // A few tokens (decoding): the recurrence itself in float32,
 //   M <- a M + k_t^T v_t,   o_t = is q_t M,
 // with the state's 64 columns of a block in registers: thread (x, y) holds
@@ -124,9 +125,16 @@ SweepPlan plan(const Sweep* a, int n) {
   }
   p.pairs = a->B * a->H;
   const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * p.vblocks * n;
-  // Two workgroups for each of the 256 CUs; segments of at least two chunks.
-  int64_t G = groups >= 256 ? 1 : (512 + groups - 1) / groups;
-  G = std::max<int64_t>(1, std::min(G, chunks / 2));
+  // Segments cost a second pass over keys and values, so they are for calls
+  // that leave CUs idle: below 160 workgroups, up to two for each of the 256
+  // CUs, of at least four chunks (float32, whose chunks take three times as
+  // long: two).  Measured, us, with 1 / 4 / 8 / 16 / 64 segments: 192
+  // workgroups (gradients, 64 chunks) 101 / 108 / 119 / 129 / 240; 64 of them
+  // (64 chunks) 155 / 77 / 73 / 78 / 116; 32 (128 chunks of K = V = 128)
+  // 301 / 139 / 88 / 81 / 121; 2 (256 chunks) 380 / 171 / 95 / 58 / 36, and
+  // 41 with 128.
+  int64_t G = groups >= 160 ? 1 : (512 + groups - 1) / groups;
+  G = std::max<int64_t>(1, std::min(G, chunks / (a->bf16 ? 4 : 2)));
   const int64_t per = (chunks + G - 1) / G;
   p.seg_tokens = (int)(per * kChunk);
   p.segments = (int)((chunks + per - 1) / per);

@@ -57,17 +57,44 @@ constexpr int kPlane = 64 * 64;
 // log2 of the decay, finite: the factor of any distance > 0 is 0 at -4096.
 __device__ __forceinline__ float log2_decay(float ld) { return ld < -2839.f ? -4096.f : ld * 1.44269504f; }
 
+// The decay over d tokens; 0 where d is negative.
+__device__ __forceinline__ float decayed(float gl, int d) {
+  const float e = ex2(gl * (d < 0 ? 0 : d));
+  return d < 0 ? 0.f : e;
+}
+
 __device__ __forceinline__ int64_t tokens_of(const Sweep& a, int64_t b) {
   if (!a.lengths) return a.T;
   const int64_t n = a.lengths[b];
   return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 
-// The rows of one chunk of a tensor: nt rows from token a0 on.
-__device__ __forceinline__ Rsrc chunk_rsrc(const Tensor& x, int64_t b, int64_t h, int64_t a0, int nt, int D, int isz) {
-  char* base = static_cast<char*>(const_cast<void*>(x.p)) + (b * x.b + h * x.h + a0 * x.t) * isz;
-  return __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)(((nt - 1) * x.t + D) * isz), wkv6::kRsrcFlags);
-}
+// A tensor's rows of one (batch item, head) as a sweep meets them, 64 at a
+// time: `at` points at the chunk's first row in memory order (before the
+// tensor's start where a reversed sweep's last chunk is short; those rows are
+// masked) and moves by a constant from chunk to chunk, so that a lane's
+// offsets never change.
+struct Rows {
+  const char* at;
+  int64_t step;   // bytes from a chunk to the next
+  int stride;     // bytes from a row to the next one of the sweep, ...
+  int base;       // ... and of row 0
+
+  __device__ __forceinline__ void start(const Tensor& x, int64_t b, int64_t h, int64_t lo, int64_t len, bool rev, int isz) {
+    const int64_t row = x.t * isz, first = rev ? len - lo - kChunk : lo;
+    at = static_cast<const char*>(x.p) + (b * x.b + h * x.h) * isz + first * row;
+    step = rev ? -kChunk * row : kChunk * row;
+    stride = rev ? -(int)row : (int)row;
+    base = rev ? (kChunk - 1) * (int)row : 0;
+  }
+  // byte offset of row j, channel c; out of range for channels behind the last
+  __device__ __forceinline__ int offset(int j, int c, int D, int isz) const {
+    return c < D ? base + j * stride + c * isz : wkv6::kOffNone;
+  }
+  __device__ __forceinline__ Rsrc rsrc() const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, wkv6::kOffNone, wkv6::kRsrcFlags);
+  }
+};
 
 // Eight adjacent channels as loaded: 16 bytes of bfloat16 or 32 of float32.
 template <bool BF>
@@ -139,18 +166,20 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   __shared__ __bf16 Vp[NI * kPlane];
   __shared__ __bf16 Sp[SUMMARY ? 8 : MP * KP * 64];
 
-  const Sweep& a = p.a[blockIdx.y];
+  // The sweeps and blocks of values of one item, which read the same rows, are
+  // 8 apart, so that they run on one XCD and share its L2.
+  const int kinds = p.vblocks * p.sweeps;
+  const int64_t item = (int64_t)(blockIdx.x / (8 * kinds)) * 8 + blockIdx.x % 8;
+  const int kind = blockIdx.x / 8 % kinds, sweep = kind / p.vblocks, vb = kind % p.vblocks;
+  const Sweep& a = p.a[sweep];
   const bool rev = a.reverse;
-  // Blocks of one item are 8 apart, so that they run on one XCD and share its L2.
-  const int64_t item = (int64_t)(blockIdx.x / (8 * p.vblocks)) * 8 + blockIdx.x % 8;
-  const int vb = (blockIdx.x / 8) % p.vblocks;
   if (item >= p.items) return;
+  const int v0 = vb * kVBlock;
+  if (v0 >= a.V) return;
   const int segs = SUMMARY ? p.segments - 1 : p.segments;
   const int64_t pair = item / segs;
   const int seg = (int)(item % segs);
   const int64_t b = pair / a.H, h = pair % a.H;
-  const int v0 = vb * kVBlock;
-  if (v0 >= a.V) return;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const float gl = log2_decay(a.log_decay[h]);
@@ -167,7 +196,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   int64_t cs = a.V, ns = 1;
   if constexpr (!SUMMARY) {
     if (p.ws)
-      s_from = p.ws + ((blockIdx.y * p.pairs + pair) * p.segments + seg) * a.K * a.V;
+      s_from = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * a.K * a.V;
     else if (a.s_in) {
       s_from = a.s_in + pair * a.K * a.V;
       if (a.s_transposed) cs = 1, ns = a.K;
@@ -189,7 +218,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int d = li - 4 * g - r;
-    dg[r] = d >= 0 ? ex2(gl * d) * a.ps : 0.f;
+    dg[r] = decayed(gl, d) * a.ps;
     of[r] = ex2(gl * (16 + d)) * a.ps;
   }
   const float a16 = ex2(gl * 16.f);
@@ -200,44 +229,55 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int d = nt - 1 + (rev ? 1 : 0) - (32 * u + 8 * g + j);
-        uf[u][j] = d >= 0 ? ex2(gl * d) * a.us : 0.f;
+        uf[u][j] = decayed(gl, d) * a.us;
       }
   };
   update_factors(kChunk);
 
-  // ---- loads: chunk c covers nt tokens from a0 on; row j in sweep order
-  Raw8<BF> kr[KR], vr[2], qr[NJ];
-  const auto load = [&](int c) {
-    const int64_t at = lo + (int64_t)c * kChunk;
-    const int nt = (int)(hi - at < kChunk ? hi - at : kChunk);
-    const int64_t a0 = rev ? len - at - nt : at;
-    const Rsrc rk = chunk_rsrc(a.k, b, h, a0, nt, a.K, ISZ), rv = chunk_rsrc(a.v, b, h, a0, nt, a.V, ISZ);
-    const auto off = [&](int j, int64_t stride, int col, int D) {
-      return j < nt && col < D ? (rev ? nt - 1 - j : j) * (int)stride * ISZ + col * ISZ : wkv6::kOffNone;
-    };
+  // ---- loads of a chunk of nt tokens (none: everything out of range)
+  Raw8<BF> kr[KR], vr[2], qr[SUMMARY ? 1 : NJ];
+  Rows rk, rv, rq, ro;
+  int ok[KR], ov[2], oq[NJ] = {}, oo[2] = {};
+  constexpr int OSZ = OBF ? 2 : 4;
+  rk.start(a.k, b, h, lo, len, rev, ISZ);
+  rv.start(a.v, b, h, lo, len, rev, ISZ);
 #pragma unroll
-    for (int x = 0; x < KR; ++x) {
-      const int id = tid + x * NTH;
-      kr[x] = load8<BF>(rk, off(id / (KP / 8), a.k.t, id % (KP / 8) * 8, a.K));
-    }
+  for (int x = 0; x < KR; ++x) ok[x] = rk.offset((tid + x * NTH) / (KP / 8), (tid + x * NTH) % (KP / 8) * 8, a.K, ISZ);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int id = tid + x * NTH;
-      vr[x] = load8<BF>(rv, off(id / 8, a.v.t, v0 + id % 8 * 8, a.V));
-    }
+  for (int x = 0; x < 2; ++x) ov[x] = rv.offset((tid + x * NTH) / 8, v0 + tid % 8 * 8, a.V, ISZ);
+  if constexpr (!SUMMARY) {
+    rq.start(a.q, b, h, lo, len, rev, ISZ);
+    ro.start(a.o, b, h, lo, len, rev, OSZ);
+#pragma unroll
+    for (int J = 0; J < NJ; ++J) oq[J] = rq.offset(16 * w + li, 32 * J + 8 * g, a.K, ISZ);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) oo[u] = ro.offset(16 * w + li, v0 + 32 * u + 8 * g, a.V, OSZ);
+  }
+  const auto load = [&](int nt) {
+    const Rsrc bk = rk.rsrc(), bv = rv.rsrc();
+#pragma unroll
+    for (int x = 0; x < KR; ++x) kr[x] = load8<BF>(bk, (tid + x * NTH) / (KP / 8) < nt ? ok[x] : wkv6::kOffNone);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) vr[x] = load8<BF>(bv, (tid + x * NTH) / 8 < nt ? ov[x] : wkv6::kOffNone);
+    rk.at += rk.step;
+    rv.at += rv.step;
     if constexpr (!SUMMARY) {
-      const Rsrc rq = chunk_rsrc(a.q, b, h, a0, nt, a.K, ISZ);
+      const Rsrc bq = rq.rsrc();
 #pragma unroll
-      for (int J = 0; J < NJ; ++J) qr[J] = load8<BF>(rq, off(16 * w + li, a.q.t, 32 * J + 8 * g, a.K));
+      for (int J = 0; J < NJ; ++J)
+        qr[J] = load8<BF>(bq, 16 * w + li < nt ? oq[J] : wkv6::kOffNone);
+      rq.at += rq.step;
     }
   };
-  if (nch > 0) load(0);
+  const auto tokens = [&](int c) {
+    const int64_t left = hi - lo - (int64_t)c * kChunk;
+    return (int)(left < 0 ? 0 : left < kChunk ? left : kChunk);
+  };
+  if (nch > 0) load(tokens(0));
 
   const bool last_seg = hi == len;
   for (int c = 0; c < nch; ++c) {
-    const int64_t at = lo + (int64_t)c * kChunk;
-    const int nt = (int)(hi - at < kChunk ? hi - at : kChunk);
-    const int64_t a0 = rev ? len - at - nt : at;
+    const int nt = tokens(c);
     // ---- keys, values and the state to LDS
 #pragma unroll
     for (int x = 0; x < KR; ++x) {
@@ -264,10 +304,11 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
       }
     }
     lds_barrier();
-    if (c + 1 < nch) load(c + 1);
+    load(tokens(c + 1));
+    __builtin_amdgcn_sched_barrier(0);   // the loads go out now
 
     if constexpr (!SUMMARY) {
-      if (16 * w < nt) {
+      {
         // ---- the state's part: O^T[n][t] = sum_c M[c][n] q_t[c]
         f32x4 acc[4];
 #pragma unroll
@@ -309,14 +350,11 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
           }
         }
         // ---- store: row t, channels v0 + 32u + 8g..+7
-        const int j = 16 * w + li;
-        constexpr int OSZ = OBF ? 2 : 4;
-        const Rsrc ro = chunk_rsrc(a.o, b, h, a0, nt, a.V, OSZ);
-        const int orow = (rev ? nt - 1 - j : j) * (int)a.o.t;
+        const Rsrc bo = ro.rsrc();
+        ro.at += ro.step;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int n = v0 + 32 * u + 8 * g;
-          const int off = j < nt && n < a.V ? (orow + n) * OSZ : wkv6::kOffNone;
+          const int off = 16 * w + li < nt ? oo[u] : wkv6::kOffNone;
           const f32x4 x = acc[2 * u], y = acc[2 * u + 1];
           if constexpr (OBF) {
             typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -324,10 +362,10 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
                              __builtin_bit_cast(unsigned int, wkv6::round_pair(x[2], x[3])),
                              __builtin_bit_cast(unsigned int, wkv6::round_pair(y[0], y[1])),
                              __builtin_bit_cast(unsigned int, wkv6::round_pair(y[2], y[3]))};
-            __builtin_amdgcn_raw_buffer_store_b128(q, ro, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(q, bo, off, 0, 0);
           } else {
-            wkv6::bstoref4(ro, off, x[0], x[1], x[2], x[3]);
-            wkv6::bstoref4(ro, off + 16, y[0], y[1], y[2], y[3]);
+            wkv6::bstoref4(bo, off, x[0], x[1], x[2], x[3]);
+            wkv6::bstoref4(bo, off + 16, y[0], y[1], y[2], y[3]);
           }
         }
       }
@@ -374,7 +412,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // ---- hand on the state
   float* s_to = nullptr;
   if constexpr (SUMMARY)
-    s_to = p.ws + ((blockIdx.y * p.pairs + pair) * p.segments + seg) * a.K * a.V;
+    s_to = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * a.K * a.V;
   else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
     s_to = a.s_out + pair * a.K * a.V;
     cs = a.s_transposed ? 1 : a.V;
@@ -394,7 +432,6 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // ---- rows behind the sequence: zero, each segment those of its own places
   if constexpr (!SUMMARY) {
     const int64_t z0 = len > lo ? len : lo, z1 = lo + p.seg_tokens < a.T ? lo + p.seg_tokens : a.T;
-    constexpr int OSZ = OBF ? 2 : 4;
     for (int64_t t = z0 + tid / 8; t < z1; t += NTH / 8) {
       const int n = v0 + tid % 8 * 8;
       if (n < a.V) {
@@ -408,6 +445,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 
 // The segments' own states, as the summaries left them, become the states
 // that enter the segments: M_0 = s_in, M_{s+1} = a^(tokens of s) M_s + U_s.
+constexpr int kAhead = 8;
 __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
   const Sweep& a = p.a[blockIdx.z];
   const int64_t pair = blockIdx.x;
@@ -418,18 +456,25 @@ __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
   const int from = a.s_transposed ? (e % a.V) * a.K + e / a.V : e;
   float m = a.s_in ? a.s_in[pair * KV + from] : 0.f;
   float* at = p.ws + (blockIdx.z * p.pairs + pair) * p.segments * KV + e;
-  for (int s = 0; s < p.segments; ++s, at += KV) {
-    const float u = s + 1 < p.segments ? *at : 0.f;
-    *at = m;
-    const int64_t lo = (int64_t)s * p.seg_tokens, left = len - lo;
-    const int64_t n = left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens;
-    m = m * ex2(gl * (float)n) + u;
+  for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
+    float u[kAhead];   // loaded together: the chain through m must not wait for memory
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) u[i] = s0 + i + 1 < p.segments ? at[(s0 + i) * (int64_t)KV] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i;
+      if (s >= p.segments) break;
+      at[s * (int64_t)KV] = m;
+      const int64_t left = len - (int64_t)s * p.seg_tokens;
+      const int64_t n = left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens;
+      m = m * ex2(gl * (float)n) + u[i];
+    }
   }
 }
 
 template <int KP, bool BF, int MP, int UP, bool OBF>
 hipError_t launch(const SweepPlan& p, hipStream_t s) {
-  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.vblocks), p.sweeps); };
+  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.vblocks * p.sweeps)); };
   if (p.segments > 1) {
     SweepPlan q = p;
     q.items = p.pairs * (p.segments - 1);
