@@ -118,13 +118,17 @@ SweepPlan plan(const Sweep* a, int n) {
   SweepPlan p = {};
   p.sweeps = n;
   p.vblocks = 1;
+  int blocks = 0, K = 0;
   for (int i = 0; i < n; ++i) {
     p.a[i] = a[i];
     p.state_out = p.state_out || a[i].s_out;
-    p.vblocks = std::max(p.vblocks, (a[i].V + kVBlock - 1) / kVBlock);
+    const int vb = (a[i].V + kVBlock - 1) / kVBlock;
+    p.vblocks = std::max(p.vblocks, vb);
+    blocks += vb;
+    K = std::max(K, a[i].K);
   }
   p.pairs = a->B * a->H;
-  const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * p.vblocks * n;
+  const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * blocks;
   // Segments cost a second pass over keys and values, so they are for calls
   // that leave CUs idle: below 160 workgroups, up to two for each of the 256
   // CUs, of at least four chunks (float32, whose chunks take three times as
@@ -132,8 +136,11 @@ SweepPlan plan(const Sweep* a, int n) {
   // workgroups (gradients, 64 chunks) 101 / 108 / 119 / 129 / 240; 64 of them
   // (64 chunks) 155 / 77 / 73 / 78 / 116; 32 (128 chunks of K = V = 128)
   // 301 / 139 / 88 / 81 / 121; 2 (256 chunks) 380 / 171 / 95 / 58 / 36, and
-  // 41 with 128.
+  // 41 with 128.  A CU holds one workgroup of the float32 sweeps of more than
+  // 64 key channels at a time, so those stay in one round of 256 (gradients
+  // of K = 128, V = 64, 13 chunks: 73 us with 3 segments, 80 with 5).
   int64_t G = groups >= 160 ? 1 : (512 + groups - 1) / groups;
+  if (!a->bf16 && K > 64 && G > 1) G = 256 / groups;
   G = std::max<int64_t>(1, std::min(G, chunks / (a->bf16 ? 4 : 2)));
   const int64_t per = (chunks + G - 1) / G;
   p.seg_tokens = (int)(per * kChunk);

@@ -119,7 +119,7 @@ __device__ __forceinline__ Op<BF ? 1 : 3> operand(const Raw8<BF>& x) {
   } else {
     float f[8];
     __builtin_memcpy(f, x.q, 32);
-    return wkv6::split8<3, false>(f);
+    return wkv6::split8<3>(f);
   }
 }
 
@@ -170,12 +170,10 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // 8 apart, so that they run on one XCD and share its L2.
   const int kinds = p.vblocks * p.sweeps;
   const int64_t item = (int64_t)(blockIdx.x / (8 * kinds)) * 8 + blockIdx.x % 8;
-  const int kind = blockIdx.x / 8 % kinds, sweep = kind / p.vblocks, vb = kind % p.vblocks;
+  const int kind = blockIdx.x / 8 % kinds, sweep = kind / p.vblocks, v0 = kind % p.vblocks * kVBlock;
   const Sweep& a = p.a[sweep];
   const bool rev = a.reverse;
-  if (item >= p.items) return;
-  const int v0 = vb * kVBlock;
-  if (v0 >= a.V) return;
+  if (item >= p.items || v0 >= a.V) return;
   const int segs = SUMMARY ? p.segments - 1 : p.segments;
   const int64_t pair = item / segs;
   const int seg = (int)(item % segs);
@@ -192,25 +190,30 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // ---- the entering state: rows c = 32J + 8g + 4e + r, column n of strip w
   f32x4 M[NJ][2];
   const int sn = v0 + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
+  // (unconditional buffer loads: a branch around each would wait for each)
+  const int KV = a.K * a.V;
+  int cs = a.V, ns = 1;
   const float* s_from = nullptr;
-  int64_t cs = a.V, ns = 1;
   if constexpr (!SUMMARY) {
-    if (p.ws)
-      s_from = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * a.K * a.V;
-    else if (a.s_in) {
-      s_from = a.s_in + pair * a.K * a.V;
+    if (p.ws) {
+      s_from = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * KV;
+    } else {
+      s_from = a.s_in ? a.s_in + pair * KV : nullptr;
       if (a.s_transposed) cs = 1, ns = a.K;
     }
   }
+  const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s_from), (short)0, s_from ? KV * 4 : 0, wkv6::kRsrcFlags);
+  const auto state_offset = [&](int J, int e, int r) {
+    const int c = 32 * J + 8 * g + 4 * e + r;
+    return c < a.K && sn < a.V ? (c * cs + sn * ns) * 4 : wkv6::kOffNone;
+  };
 #pragma unroll
   for (int J = 0; J < NJ; ++J)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int c = 32 * J + 8 * g + 4 * e + r;
-        M[J][e][r] = s_from && c < a.K && sn < a.V ? s_from[c * cs + sn * ns] : 0.f;
-      }
+      for (int r = 0; r < 4; ++r)
+        M[J][e][r] = SUMMARY ? 0.f : __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(J, e, r), 0, 0));
 
   // ---- factors of whole chunks
   const float f_inter = ex2(gl * (16 * w + li + (rev ? 0 : 1))) * a.is;   // column t = 16w + li
@@ -297,7 +300,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = M[J][e >> 2][e & 3];
-        const Op<MP> o = wkv6::split8<MP, false>(f);
+        const Op<MP> o = wkv6::split8<MP>(f);
 #pragma unroll
         for (int s = 0; s < MP; ++s)
           *reinterpret_cast<bf16x8*>(Sp + ((s * 4 + w) * NJ + J) * 512 + lane * 8) = o.p[s];
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 #pragma unroll
               for (int r = 0; r < 4; ++r) pr[4 * e + r] = sc[r];
             }
-            const Op<MP> pf = wkv6::split8<MP, false>(pr);
+            const Op<MP> pf = wkv6::split8<MP>(pr);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               const int row = 32 * u + 4 * g + (li >> 2), col = 4 * (s >> 1) + (li & 3);
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
             if constexpr (NI == 3) f[j] += (float)vo.p[1][j] + (float)vo.p[2][j];
             f[j] *= uf[u][j];
           }
-          const Op<UP> vf = wkv6::split8<UP, false>(f);
+          const Op<UP> vf = wkv6::split8<UP>(f);
 #pragma unroll
           for (int J = 0; J < NJ; ++J)
 #pragma unroll
@@ -411,23 +414,23 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 
   // ---- hand on the state
   float* s_to = nullptr;
-  if constexpr (SUMMARY)
-    s_to = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * a.K * a.V;
-  else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
-    s_to = a.s_out + pair * a.K * a.V;
+  if constexpr (SUMMARY) {
+    s_to = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * KV;
+  } else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
+    s_to = a.s_out + pair * KV;
     cs = a.s_transposed ? 1 : a.V;
     ns = a.s_transposed ? a.K : 1;
   }
-  if (s_to)
+  if (s_to) {
+    const Rsrc rt = __builtin_amdgcn_make_buffer_rsrc(s_to, (short)0, KV * 4, wkv6::kRsrcFlags);
 #pragma unroll
     for (int J = 0; J < NJ; ++J)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int c = 32 * J + 8 * g + 4 * e + r;
-          if (c < a.K && sn < a.V) s_to[c * cs + sn * ns] = M[J][e][r];
-        }
+        for (int r = 0; r < 4; ++r)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(M[J][e][r]), rt, state_offset(J, e, r), 0, 0);
+  }
 
   // ---- rows behind the sequence: zero, each segment those of its own places
   if constexpr (!SUMMARY) {
@@ -459,7 +462,7 @@ __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
   for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
     float u[kAhead];   // loaded together: the chain through m must not wait for memory
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) u[i] = s0 + i + 1 < p.segments ? at[(s0 + i) * (int64_t)KV] : 0.f;
+    for (int i = 0; i < kAhead; ++i) u[i] = at[min(s0 + i, p.segments - 1) * (int64_t)KV];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int s = s0 + i;
@@ -467,7 +470,7 @@ __global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
       at[s * (int64_t)KV] = m;
       const int64_t left = len - (int64_t)s * p.seg_tokens;
       const int64_t n = left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens;
-      m = m * ex2(gl * (float)n) + u[i];
+      m = m * ex2(gl * (float)n) + u[i];   // (not used after the last segment)
     }
   }
 }
