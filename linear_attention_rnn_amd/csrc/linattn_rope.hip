@@ -20,7 +20,9 @@ namespace linattn {
 namespace {
 
 constexpr int NTR = 256;
-constexpr int kMaxAngles = 1024;   // tokens of a workgroup times R / 2
+constexpr int kMaxTokens = 16;     // of a workgroup
+constexpr int kMaxAngles = 1024;   // those times R / 2
+constexpr int kTogether = 4;       // tokens whose loads a thread has in flight
 
 __device__ __forceinline__ float2 turn_of(double angle, bool inverse) {
   constexpr double kInv2Pi = 0.15915494309189535;       // 1 / (2 pi), rounded
@@ -77,13 +79,19 @@ __device__ __forceinline__ void put(void* p, int64_t i, const float (&x)[N]) {
 template <bool BF, bool INTER, int N>
 __global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens, int rows_share) {
   __shared__ float2 cs[kMaxAngles];
+  __shared__ int64_t base[4][kMaxTokens];   // of a token's rows in q, k, q_out, k_out
   const int half = a.R / 2, tid = threadIdx.x;
   const int64_t n = a.B * a.T, first = (int64_t)blockIdx.x * tokens;
   const int nt = (int)(n - first < tokens ? n - first : tokens);
   for (int e = tid; e < nt * half; e += NTR) {
-    const int64_t tok = first + e / half;
-    const int64_t pos = a.start + (a.positions ? (int64_t)a.positions[tok] : tok % a.T);
+    const uint32_t tok = (uint32_t)first + e / half;
+    const int64_t pos = a.start + (a.positions ? a.positions[tok] : (int32_t)(tok % (uint32_t)a.T));
     cs[e] = turn_of((double)pos * a.freqs[e % half], a.inverse);
+  }
+  for (int e = tid; e < 4 * nt; e += NTR) {
+    const uint32_t tok = (uint32_t)first + e / 4, T = (uint32_t)a.T, b = tok / T, t = tok % T;   // fewer than 2^27 tokens
+    const Tensor& x = e % 4 == 0 ? a.q : e % 4 == 1 ? a.k : e % 4 == 2 ? a.q_out : a.k_out;
+    base[e % 4][e / 4] = b * x.b + t * x.t;
   }
   __syncthreads();
   // pieces of a row: those that turn, then those that are copied
@@ -91,43 +99,52 @@ __global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens, int rows_
   const int per = NTR / units, u = tid % units, slot = tid / units;
   if (slot >= per) return;
   const int all = a.k.p ? 2 * (int)a.H : (int)a.H, r0 = blockIdx.y * rows_share;
-  const int rows = all - r0 < rows_share ? all - r0 : rows_share;
-  for (int row = slot; row < nt * rows; row += per) {
-    const int ti = row / rows, r = r0 + row % rows;
-    const int64_t tok = first + ti, b = tok / a.T, t = tok % a.T;
+  const int rows = all - r0 < rows_share ? all : r0 + rows_share;
+  const bool copy = u >= turning;
+  const int c = copy ? a.R + N * (u - turning) : N * u;
+  for (int r = r0 + slot; r < rows; r += per) {
     const bool isk = r >= a.H;
-    const int64_t h = isk ? r - a.H : r;
     const Tensor& x = isk ? a.k : a.q;
     const Tensor& y = isk ? a.k_out : a.q_out;
-    const int64_t from = b * x.b + t * x.t + h * x.h, to = b * y.b + t * y.t + h * y.h;
-    void* out = const_cast<void*>(y.p);
-    float p[N], q[N];
-    if (u >= turning) {
-      const int c = a.R + N * (u - turning);
-      get<BF>(x.p, from + c, p);
-      put<BF>(out, to + c, p);
-    } else if constexpr (INTER) {
-      get<BF>(x.p, from + N * u, p);
+    const int64_t h = isk ? r - a.H : r, from = h * x.h + c, to = h * y.h + c;
+    const int64_t* const fb = base[isk ? 1 : 0];
+    const int64_t* const tb = base[isk ? 3 : 2];
+    void* const out = const_cast<void*>(y.p);
+    // kTogether tokens at a time, all of their loads before the first store
+    for (int t0 = 0; t0 < nt; t0 += kTogether) {
+      float p[kTogether][N], q[INTER ? 1 : kTogether][N];
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        const float2 e = cs[ti * half + N / 2 * u + j];
-        const float v = p[2 * j], z = p[2 * j + 1];
-        p[2 * j] = v * e.x - z * e.y;
-        p[2 * j + 1] = v * e.y + z * e.x;
+      for (int i = 0; i < kTogether; ++i) {
+        const int ti = min(t0 + i, nt - 1);
+        get<BF>(x.p, fb[ti] + from, p[i]);
+        if constexpr (!INTER) get<BF>(x.p, fb[ti] + from + (copy ? 0 : half), q[i]);
       }
-      put<BF>(out, to + N * u, p);
-    } else {
-      get<BF>(x.p, from + N * u, p);
-      get<BF>(x.p, from + half + N * u, q);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float2 e = cs[ti * half + N * u + j];
-        const float v = p[j];
-        p[j] = v * e.x - q[j] * e.y;
-        q[j] = v * e.y + q[j] * e.x;
+      for (int i = 0; i < kTogether; ++i) {
+        const int ti = t0 + i;
+        if (ti >= nt) break;
+        if (!copy) {
+          if constexpr (INTER) {
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+              const float2 e = cs[ti * half + N / 2 * u + j];
+              const float v = p[i][2 * j], z = p[i][2 * j + 1];
+              p[i][2 * j] = v * e.x - z * e.y;
+              p[i][2 * j + 1] = v * e.y + z * e.x;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+              const float2 e = cs[ti * half + N * u + j];
+              const float v = p[i][j];
+              p[i][j] = v * e.x - q[i][j] * e.y;
+              q[i][j] = v * e.y + q[i][j] * e.x;
+            }
+            put<BF>(out, tb[ti] + to + half, q[i]);
+          }
+        }
+        put<BF>(out, tb[ti] + to, p[i]);
       }
-      put<BF>(out, to + N * u, p);
-      put<BF>(out, to + half + N * u, q);
     }
   }
 }
@@ -145,7 +162,7 @@ hipError_t enqueue_rope(const Rope& a, hipStream_t s) {
   const int64_t rows = a.k.p ? 2 * a.H : a.H;
   // Sixteen tokens a workgroup, fewer where the angles would not fit or the
   // card would not be filled; a token's rows are shared out if there are few.
-  int tokens = 16;
+  int tokens = kMaxTokens;
   while (tokens > 1 && (tokens * (a.R / 2) > kMaxAngles || n / tokens < 1024)) tokens /= 2;
   int64_t shares = 1;
   const int64_t groups = (n + tokens - 1) / tokens;
