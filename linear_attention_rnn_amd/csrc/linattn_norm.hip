@@ -42,6 +42,35 @@ __device__ __forceinline__ void get8(const void* p, int64_t i, float (&x)[8]) {
   }
 }
 
+// Eight values as loaded, so that rows to come take few registers.
+template <bool BF>
+struct Raw8 {
+  uint4 q[BF ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (BF ? 2 : 4));
+    q[0] = at[0];
+    if constexpr (!BF) q[1] = at[1];
+  }
+  __device__ __forceinline__ void clear() {
+    q[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (!BF) q[1] = q[0];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF) {
+        x[2 * j] = __uint_as_float(u[j] << 16);
+        x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      } else {
+        const uint32_t v[4] = {q[BF ? 0 : 1].x, q[BF ? 0 : 1].y, q[BF ? 0 : 1].z, q[BF ? 0 : 1].w};
+        x[j] = __uint_as_float(u[j]);
+        x[4 + j] = __uint_as_float(v[j]);
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ uint32_t pair(float a, float b) {   // bfloat16, nearest even
   typedef float f2 __attribute__((ext_vector_type(2)));
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
@@ -210,23 +239,38 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     for (int j = 0; j < 8; ++j) dw[v][j] = wt[v][j] = 0.f;
     if (c < a.C) get8<false>(a.weight, c, wt[v]);
   }
-  int turn = 0;
-  // every wave of a workgroup makes the same turns where rows are shared by waves (RW == 1)
-  for (int64_t row = (int64_t)blockIdx.x * RW + slot; row < a.rows; row += (int64_t)gridDim.x * RW, turn ^= 1) {
-    const int64_t base = row * a.C;
-    float h[NV][8], d[NV][8];
-    float hh = 0.f, hd = 0.f;
+  // The next row's loads go out before the present one is worked on.
+  Raw8<BF> hn[NV], dn[NV], en[NV];
+  const auto load = [&](int64_t row) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;
-      if (c < a.C) {
-        get8<BF>(a.h, base + c, h[v]);
-        get8<BF>(a.dy, base + c, d[v]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[v][j] = d[v][j] = 0.f;
+      const int64_t i = row * a.C + c;
+      hn[v].clear();
+      dn[v].clear();
+      en[v].clear();
+      if (row < a.rows && c < a.C) {
+        hn[v].load(a.h, i);
+        dn[v].load(a.dy, i);
+        if (a.dh) en[v].load(a.dh, i);
       }
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RW;
+  int64_t row = (int64_t)blockIdx.x * RW + slot;
+  load(row);
+  // every wave of a workgroup makes the same turns where rows are shared by waves (RW == 1)
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    const int64_t base = row * a.C;
+    float h[NV][8], d[NV][8], x[NV][8];
+    float hh = 0.f, hd = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      hn[v].get(h[v]);
+      dn[v].get(d[v]);
+      en[v].get(x[v]);
+    }
+    load(row + step);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -241,19 +285,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;
-      if (c >= a.C) continue;
-      float x[8];
-      if (a.dh)
-        get8<BF>(a.dh, base + c, x);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[v][j] = fmaf(d[v][j], h[v][j] * r, dw[v][j]);
-        x[j] = fmaf(r, d[v][j] * wt[v][j] - h[v][j] * f, x[j]);
+        x[v][j] = fmaf(r, d[v][j] * wt[v][j] - h[v][j] * f, x[v][j]);
       }
-      put8<BF>(a.dx, base + c, x);
+      if (c < a.C) put8<BF>(a.dx, base + c, x[v]);
     }
   }
   if constexpr (RW > 1) {
@@ -282,19 +319,26 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     }
 }
 
-// dweight[c] = the workgroups' sums, in 16 interleaved shares.
-__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, float* dweight, int groups, int64_t C) {
-  __shared__ float lds[16][65];
-  const int c = threadIdx.x % 64, s = threadIdx.x / 64;
-  const int64_t col = (int64_t)blockIdx.x * 64 + c;
-  float x = 0.f;
+// dweight of 16 columns: the workgroups' sums in 64 interleaved shares, the
+// shares in order.
+__global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, float* dweight, int groups, int64_t C) {
+  __shared__ float lds[64][16];
+  const int q = threadIdx.x % 4, s = threadIdx.x / 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + 4 * q;   // C is a multiple of 8
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < C)
-    for (int i = s; i < groups; i += 16) x += part[i * C + col];
-  lds[s][c] = x;
+#pragma unroll 8
+    for (int i = s; i < groups; i += 64) {
+      const float4 y = *reinterpret_cast<const float4*>(part + i * C + col);
+      x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+  *reinterpret_cast<float4*>(&lds[s][4 * q]) = x;
   __syncthreads();
-  if (s == 0 && col < C) {
-    for (int i = 1; i < 16; ++i) x += lds[i][c];
-    dweight[col] = x;
+  if (threadIdx.x < 16 && (int64_t)blockIdx.x * 16 + threadIdx.x < C) {
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) y += lds[i][threadIdx.x];
+    dweight[(int64_t)blockIdx.x * 16 + threadIdx.x] = y;
   }
 }
 
@@ -309,6 +353,15 @@ struct Shape {
 Shape shape_of(int64_t rows, int64_t C) {
   const int64_t pieces = C / 8;
   const int tpr = pieces <= 64 || (pieces <= 256 && rows >= 2048) ? 64 : pieces <= 1024 ? 256 : 512;
+  const int64_t need = (pieces + tpr - 1) / tpr;
+  return {tpr, need <= 1 ? 1 : need <= 2 ? 2 : 4};
+}
+
+// The gradients keep the next row and the sums of dweight besides: at most two
+// pieces a thread up to 8192 columns.
+Shape bwd_shape_of(int64_t rows, int64_t C) {
+  const int64_t pieces = C / 8;
+  const int tpr = pieces <= 64 || (pieces <= 128 && rows >= 2048) ? 64 : pieces <= 512 ? 256 : 512;
   const int64_t need = (pieces + tpr - 1) / tpr;
   return {tpr, need <= 1 ? 1 : need <= 2 ? 2 : 4};
 }
@@ -340,40 +393,26 @@ int bwd_groups(const NormBwd& a, const Shape& f) {
 
 }  // namespace
 
-// call(TPR, NV) for the shape f (512 threads: more than 8192 columns)
-#define LINATTN_SHAPES(call)             \
-  if (f.tpr == 64) {                     \
-    if (f.nv == 1) call(64, 1);          \
-    else if (f.nv == 2) call(64, 2);     \
-    else call(64, 4);                    \
-  } else if (f.tpr == 256) {             \
-    if (f.nv == 1) call(256, 1);         \
-    else if (f.nv == 2) call(256, 2);    \
-    else call(256, 4);                   \
-  } else {                               \
-    call(512, 4);                        \
-  }
-
 hipError_t enqueue_norm(const Norm& a, hipStream_t s) {
   const Shape f = shape_of(a.rows, a.C);
-#define LINATTN_CALL(T, N) launch_norm<T, N>(a, s)
-  LINATTN_SHAPES(LINATTN_CALL)
-#undef LINATTN_CALL
+  const auto launch = f.tpr == 64    ? (f.nv == 1 ? launch_norm<64, 1> : f.nv == 2 ? launch_norm<64, 2> : launch_norm<64, 4>)
+                      : f.tpr == 256 ? (f.nv == 1 ? launch_norm<256, 1> : f.nv == 2 ? launch_norm<256, 2> : launch_norm<256, 4>)
+                                     : launch_norm<512, 4>;
+  launch(a, s);
   return hipGetLastError();
 }
 
-size_t norm_bwd_workspace_bytes(const NormBwd& a) { return (size_t)bwd_groups(a, shape_of(a.rows, a.C)) * a.C * 4; }
+size_t norm_bwd_workspace_bytes(const NormBwd& a) { return (size_t)bwd_groups(a, bwd_shape_of(a.rows, a.C)) * a.C * 4; }
 
 hipError_t enqueue_norm_bwd(const NormBwd& a, void* workspace, hipStream_t s) {
-  const Shape f = shape_of(a.rows, a.C);
+  const Shape f = bwd_shape_of(a.rows, a.C);
   const int groups = bwd_groups(a, f);
   float* part = static_cast<float*>(workspace);
-  if (groups) {
-#define LINATTN_CALL(T, N) launch_norm_bwd<T, N>(a, part, groups, s)
-    LINATTN_SHAPES(LINATTN_CALL)
-#undef LINATTN_CALL
-  }
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.C + 63) / 64)), dim3(1024), 0, s, part, a.dweight, groups, a.C);
+  const auto launch = f.tpr == 64    ? (f.nv == 1 ? launch_norm_bwd<64, 1> : launch_norm_bwd<64, 2>)
+                      : f.tpr == 256 ? (f.nv == 1 ? launch_norm_bwd<256, 1> : launch_norm_bwd<256, 2>)
+                                     : (f.nv <= 2 ? launch_norm_bwd<512, 2> : launch_norm_bwd<512, 4>);
+  if (groups) launch(a, part, groups, s);
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.C + 15) / 16)), dim3(256), 0, s, part, a.dweight, groups, a.C);
   return hipGetLastError();
 }
 
