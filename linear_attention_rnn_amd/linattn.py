@@ -6,11 +6,12 @@ computation runs in the library's HIP kernels, PyTorch provides device memory
 and the current HIP stream, and there is no fallback.  Calls run on the
 inputs' GPU whichever device is current.
 
-Calls on torch's current stream can be captured in a HIP graph
-(``torch.cuda.graph``): while it records, workspace comes from torch's
-allocator, outside of that from the library's pool.  A call that is recorded
-on another stream is given its ``workspace`` (a uint8 tensor of at least
-``fwd_workspace_bytes`` / ``bwd_workspace_bytes`` bytes).
+Calls on torch's current stream take their workspace from torch's allocator
+(a call of the library's pool costs the host 11 us, torch's 1.3) and can be
+captured in a HIP graph (``torch.cuda.graph``).  Calls with a ``stream`` of
+their own take it from the library's pool; to be recorded there they are given
+a ``workspace``, a uint8 tensor of at least ``fwd_workspace_bytes`` /
+``bwd_workspace_bytes`` bytes.
 """
 from __future__ import annotations
 
@@ -143,18 +144,22 @@ def _call(name, f, device, stream, *args):
 
 def _workspace(given, need, device, stream):
     """(address, bytes, tensor kept alive) of a call's workspace; need() gives
-    its bytes.  Nothing, unless it was given or the current stream records a
-    graph: then the library's pool serves."""
+    its bytes.  Nothing where the library's pool serves (a stream of the
+    caller's) or none is needed."""
     if given is not None:
         if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
         return given.data_ptr(), given.numel(), given
-    if stream is None and torch.cuda.is_current_stream_capturing():
+    if stream is None:
         n = need()
         if n:
             t = torch.empty(n, dtype=torch.uint8, device=device)
             return t.data_ptr(), n, t
-    return 0, 0, None
+    return _NO_WORKSPACE
+
+
+_NO_WORKSPACE = (0, 0, None)
+_STEP_TOKENS = 8   # fwd calls of at most so many tokens take no workspace
 
 
 def _attention(q, k, v, log_decay, lengths):
@@ -202,7 +207,7 @@ def fwd(q, k, v, log_decay, scale: float = 1.0, lengths=None, s_in=None, want_st
         s_out = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
     po = _flat(s_out, "s_out", (B, H, K, V), torch.float32, dev)
     L = lib()
-    pw, nw, keep = _workspace(
+    pw, nw, keep = _NO_WORKSPACE if T <= _STEP_TOKENS else _workspace(
         workspace, lambda: L.linattn_fwd_workspace_bytes(B, T, H, K, V, dtype, odt, po != 0), dev, stream)
     _call("linattn_fwd", L.linattn_fwd, dev, stream, B, T, H, K, V, pq, pk, pv, pg, scale, pl, ps, py, po,
           _strides(q, k, v, out), dtype, odt, pw, nw)
