@@ -95,7 +95,7 @@ int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
 
 /* Workspace of a linattn_fwd call (0: none, or the arguments are invalid):
  * states at the starts of the segments that a long call over few heads is cut
- * into, B*H*segments*K*V*4 bytes (rounded up).  `state_out`: s_out is given. */
+ * into, B*H*segments*K*V*4 bytes (K and V rounded up to 64 or 128).  `state_out`: s_out is given. */
 size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, int dtype, int out_dtype,
                                    int state_out);
 

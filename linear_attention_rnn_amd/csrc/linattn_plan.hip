@@ -114,18 +114,24 @@ hipError_t launch_steps(const Sweep& a, hipStream_t s) {
 
 bool steps(const Sweep* a, int n) { return n == 1 && a->T <= kStepTokens && !a->reverse && !a->s_transposed; }
 
+// The most key channels of the sweeps: they run with 64 or 128 for all.
+int widest(const Sweep* a, int n) {
+  int K = 0;
+  for (int i = 0; i < n; ++i) K = std::max(K, a[i].K);
+  return K;
+}
+
 SweepPlan plan(const Sweep* a, int n) {
   SweepPlan p = {};
   p.sweeps = n;
   p.vblocks = 1;
-  int blocks = 0, K = 0;
+  int blocks = 0;
   for (int i = 0; i < n; ++i) {
     p.a[i] = a[i];
     p.state_out = p.state_out || a[i].s_out;
     const int vb = (a[i].V + kVBlock - 1) / kVBlock;
     p.vblocks = std::max(p.vblocks, vb);
     blocks += vb;
-    K = std::max(K, a[i].K);
   }
   p.pairs = a->B * a->H;
   const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * blocks;
@@ -140,7 +146,7 @@ SweepPlan plan(const Sweep* a, int n) {
   // 64 key channels at a time, so those stay in one round of 256 (gradients
   // of K = 128, V = 64, 13 chunks: 73 us with 3 segments, 80 with 5).
   int64_t G = groups >= 160 ? 1 : (512 + groups - 1) / groups;
-  if (!a->bf16 && K > 64 && G > 1) G = 256 / groups;
+  if (!a->bf16 && widest(a, n) > 64 && G > 1) G = 256 / groups;
   G = std::max<int64_t>(1, std::min(G, chunks / (a->bf16 ? 4 : 2)));
   const int64_t per = (chunks + G - 1) / G;
   p.seg_tokens = (int)(per * kChunk);
@@ -163,16 +169,14 @@ size_t sweep_workspace_bytes(const Sweep* a, int n) {
   if (steps(a, n)) return 0;
   const SweepPlan p = plan(a, n);
   if (p.segments == 1) return 0;
-  return ((size_t)n * p.items * a->K * a->V * 4 + 255) / 256 * 256;
+  return (size_t)n * p.items * (widest(a, n) <= 64 ? 64 : 128) * kVBlock * p.vblocks * 4;
 }
 
 hipError_t enqueue_sweeps(const Sweep* a, int n, void* workspace, hipStream_t s) {
   if (steps(a, n)) return a->K <= 64 ? launch_steps<4>(*a, s) : launch_steps<8>(*a, s);
   SweepPlan p = plan(a, n);
   if (p.segments > 1) p.ws = static_cast<float*>(workspace);
-  int K = 0;
-  for (int i = 0; i < n; ++i) K = std::max(K, a[i].K);
-  const auto launch = K <= 64 ? launch_sweeps64 : launch_sweeps128;
+  const auto launch = widest(a, n) <= 64 ? launch_sweeps64 : launch_sweeps128;
   // A sweep that leaves its state where another one takes its own from goes
   // last, after it (with segments, all states are read before the sweeps).
   bool after = false;

@@ -150,6 +150,15 @@ __device__ __forceinline__ Op<S> read_tr(const __bf16* p, int stride, int o0, in
   return o;
 }
 
+// Where a segment's state lies in the workspace: the wave's accumulators as
+// they are, [block of values][wave][J][e][lane][r], so that a lane moves 16
+// bytes at a time (element by element, 32 loads of a 128 x 64 state took as
+// long as a chunk).
+template <int KP>
+__device__ __forceinline__ int64_t segment_state(const SweepPlan& p, int sweep, int64_t pair, int seg) {
+  return ((sweep * p.pairs + pair) * p.segments + seg) * (KP * kVBlock * p.vblocks);
+}
+
 template <int KP, bool BF, int MP>
 constexpr int occupancy() {
   return KP == 64 ? (BF && MP == 1 ? 3 : 2) : (BF ? 2 : 1);
@@ -170,7 +179,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // 8 apart, so that they run on one XCD and share its L2.
   const int kinds = p.vblocks * p.sweeps;
   const int64_t item = (int64_t)(blockIdx.x / (8 * kinds)) * 8 + blockIdx.x % 8;
-  const int kind = blockIdx.x / 8 % kinds, sweep = kind / p.vblocks, v0 = kind % p.vblocks * kVBlock;
+  const int kind = blockIdx.x / 8 % kinds, sweep = kind / p.vblocks, vb = kind % p.vblocks, v0 = vb * kVBlock;
   const Sweep& a = p.a[sweep];
   const bool rev = a.reverse;
   if (item >= p.items || v0 >= a.V) return;
@@ -190,30 +199,33 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // ---- the entering state: rows c = 32J + 8g + 4e + r, column n of strip w
   f32x4 M[NJ][2];
   const int sn = v0 + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
-  // (unconditional buffer loads: a branch around each would wait for each)
   const int KV = a.K * a.V;
-  int cs = a.V, ns = 1;
-  const float* s_from = nullptr;
-  if constexpr (!SUMMARY) {
-    if (p.ws) {
-      s_from = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * KV;
-    } else {
-      s_from = a.s_in ? a.s_in + pair * KV : nullptr;
-      if (a.s_transposed) cs = 1, ns = a.K;
-    }
-  }
-  const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s_from), (short)0, s_from ? KV * 4 : 0, wkv6::kRsrcFlags);
+  const int cs = a.s_transposed ? 1 : a.V, ns = a.s_transposed ? a.K : 1;
   const auto state_offset = [&](int J, int e, int r) {
     const int c = 32 * J + 8 * g + 4 * e + r;
     return c < a.K && sn < a.V ? (c * cs + sn * ns) * 4 : wkv6::kOffNone;
   };
+  float* const seg_state = p.ws ? p.ws + segment_state<KP>(p, sweep, pair, seg) + ((vb * 4 + w) * NJ * 2 * 64 + lane) * 4 : nullptr;
+  if constexpr (SUMMARY) {
 #pragma unroll
-  for (int J = 0; J < NJ; ++J)
+    for (int J = 0; J < NJ; ++J) M[J][0] = M[J][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else if (seg_state) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int J = 0; J < NJ; ++J)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        M[J][e][r] = SUMMARY ? 0.f : __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(J, e, r), 0, 0));
+      for (int e = 0; e < 2; ++e) M[J][e] = *reinterpret_cast<const f32x4*>(seg_state + (2 * J + e) * 256);
+  } else {
+    // (unconditional buffer loads: a branch around each would wait for each)
+    const float* s_from = a.s_in ? a.s_in + pair * KV : nullptr;
+    const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s_from), (short)0, s_from ? KV * 4 : 0, wkv6::kRsrcFlags);
+#pragma unroll
+    for (int J = 0; J < NJ; ++J)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          M[J][e][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(J, e, r), 0, 0));
+  }
 
   // ---- factors of whole chunks
   const float f_inter = ex2(gl * (16 * w + li + (rev ? 0 : 1))) * a.is;   // column t = 16w + li
@@ -413,16 +425,13 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   }
 
   // ---- hand on the state
-  float* s_to = nullptr;
   if constexpr (SUMMARY) {
-    s_to = p.ws + ((sweep * p.pairs + pair) * p.segments + seg) * KV;
+#pragma unroll
+    for (int J = 0; J < NJ; ++J)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4*>(seg_state + (2 * J + e) * 256) = M[J][e];
   } else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
-    s_to = a.s_out + pair * KV;
-    cs = a.s_transposed ? 1 : a.V;
-    ns = a.s_transposed ? a.K : 1;
-  }
-  if (s_to) {
-    const Rsrc rt = __builtin_amdgcn_make_buffer_rsrc(s_to, (short)0, KV * 4, wkv6::kRsrcFlags);
+    const Rsrc rt = __builtin_amdgcn_make_buffer_rsrc(a.s_out + pair * KV, (short)0, KV * 4, wkv6::kRsrcFlags);
 #pragma unroll
     for (int J = 0; J < NJ; ++J)
 #pragma unroll
@@ -449,28 +458,39 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 // The segments' own states, as the summaries left them, become the states
 // that enter the segments: M_0 = s_in, M_{s+1} = a^(tokens of s) M_s + U_s.
 constexpr int kAhead = 8;
-__global__ __launch_bounds__(NTH) void carry_kernel(SweepPlan p) {
+constexpr int kCarryThreads = 128;
+template <int KP>
+__global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
   const Sweep& a = p.a[blockIdx.z];
   const int64_t pair = blockIdx.x;
-  const int e = blockIdx.y * NTH + threadIdx.x, KV = a.K * a.V;
-  if (e >= KV) return;
+  const int i4 = blockIdx.y * kCarryThreads + threadIdx.x, size = KP * kVBlock * p.vblocks;   // 4 adjacent of `size` elements
   const int64_t len = tokens_of(a, pair / a.H);
   const float gl = log2_decay(a.log_decay[pair % a.H]);
-  const int from = a.s_transposed ? (e % a.V) * a.K + e / a.V : e;
-  float m = a.s_in ? a.s_in[pair * KV + from] : 0.f;
-  float* at = p.ws + (blockIdx.z * p.pairs + pair) * p.segments * KV + e;
-  for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
-    float u[kAhead];   // loaded together: the chain through m must not wait for memory
+  f32x4 m = {0.f, 0.f, 0.f, 0.f};
+  if (a.s_in) {
+    const int lane = i4 & 63, g = lane >> 4, li = lane & 15, t = i4 >> 6;
+    const int e = t & 1, J = t / 2 % (KP / 32), w = t / (KP / 16) & 3, vb = t / (KP / 4);
+    const int c = 32 * J + 8 * g + 4 * e, n = vb * kVBlock + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
+    const float* s = a.s_in + pair * a.K * a.V + (a.s_transposed ? n * a.K + c : c * a.V + n);
+    if (c < a.K && n < a.V)   // K is a multiple of 8
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) u[i] = at[min(s0 + i, p.segments - 1) * (int64_t)KV];
+      for (int r = 0; r < 4; ++r) m[r] = s[a.s_transposed ? r : r * a.V];
+  }
+  f32x4* at = reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, blockIdx.z, pair, 0)) + i4;
+  const int64_t next = size / 4;
+  for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
+    f32x4 u[kAhead];   // loaded together: the chain through m must not wait for memory
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (s0 + i + 1 < p.segments) u[i] = at[(s0 + i) * next];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int s = s0 + i;
       if (s >= p.segments) break;
-      at[s * (int64_t)KV] = m;
+      at[s * next] = m;
       const int64_t left = len - (int64_t)s * p.seg_tokens;
       const int64_t n = left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens;
-      m = m * ex2(gl * (float)n) + u[i];   // (not used after the last segment)
+      if (s + 1 < p.segments) m = m * ex2(gl * (float)n) + u[i];
     }
   }
 }
@@ -481,9 +501,9 @@ hipError_t launch(const SweepPlan& p, hipStream_t s) {
   if (p.segments > 1) {
     SweepPlan q = p;
     q.items = p.pairs * (p.segments - 1);
-    const unsigned parts = (unsigned)((p.a[0].K * p.a[0].V + NTH - 1) / NTH);
+    const unsigned parts = (unsigned)(KP * kVBlock * p.vblocks / (4 * kCarryThreads));
     hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, true>), grid(q.items), dim3(NTH), 0, s, q);
-    hipLaunchKernelGGL(carry_kernel, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(NTH), 0, s, p);
+    hipLaunchKernelGGL(carry_kernel<KP>, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(kCarryThreads), 0, s, p);
   }
   hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, false>), grid(p.items), dim3(NTH), 0, s, p);
   return hipGetLastError();
