@@ -57,11 +57,13 @@ extern "C" {
  * longer ones run in chunks of 64 tokens on matrix cores.
  *
  *   B, T, H, K, V   batch, tokens, heads, key and value channels of a head;
- *             K and V are multiples of 8 from 8 to 128 (else UNSUPPORTED).
+ *             K and V are multiples of 8 from 8 to 128, B * H is at most 2^21
+ *             (else UNSUPPORTED).
  *   q, k      [B, T, H, K] of `dtype` (WKV6_DTYPE_F32 or WKV6_DTYPE_BF16)
  *   v         [B, T, H, V] of `dtype`
  *   log_decay H float32 values: the natural logarithms of the decays.
- *             Finite, or -inf (a = 0: each token sees itself alone).
+ *             Finite, or -inf (a = 0: each token sees itself alone).  Above 0
+ *             the state grows: a^64 has to be a finite float32 (1.38 at most).
  *   scale     factor of every output
  *   lengths   NULL, or B int32 values on the device: item b has
  *             min(max(lengths[b], 0), T) tokens.  The rows of q, k and v

@@ -166,10 +166,10 @@ int check_sizes(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, int dtype
   if (K < 8 || V < 8 || K > LINATTN_MAX_HEAD || V > LINATTN_MAX_HEAD || K % 8 || V % 8)
     return unsupported("K and V must be multiples of 8 from 8 to 128");
   if (B == 0) return WKV6_OK;
-  // a launch holds fewer than 2^32 work-items: (batch, head) pairs, segments
-  // and blocks of values times 256
-  if (H > (1 << 22) || B > (1 << 22) / H)
-    return unsupported("B * H exceeds the supported number of (batch, head) pairs (2^22)");
+  // a launch holds fewer than 2^32 work-items: 256 for each (batch, head) pair,
+  // block of values (two) and sweep (three for the gradients)
+  if (H > (1 << 21) || B > (1 << 21) / H)
+    return unsupported("B * H exceeds the supported number of (batch, head) pairs (2^21)");
   if (T > INT_MAX - linattn::kChunk) return unsupported("T exceeds the supported range");
   return WKV6_OK;
 }

@@ -55,8 +55,8 @@ CONTIGUOUS = [9 * 128, 128, 64] * 4
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(dtype=2), INVALID),
     (dict(out=7), INVALID), (dict(dtype=0, out=1), UNSUPPORTED), (dict(K=0), UNSUPPORTED), (dict(K=60), UNSUPPORTED),
-    (dict(V=136), UNSUPPORTED), (dict(K=256), UNSUPPORTED), (dict(B=2 ** 22, H=2), UNSUPPORTED),
-    (dict(B=2 ** 62, H=2 ** 20), UNSUPPORTED), (dict(T=2 ** 31), UNSUPPORTED),
+    (dict(V=136), UNSUPPORTED), (dict(K=256), UNSUPPORTED), (dict(B=2 ** 21 + 1, H=1), UNSUPPORTED),
+    (dict(B=2 ** 10 + 1, H=2 ** 11), UNSUPPORTED), (dict(B=2 ** 62, H=2 ** 20), UNSUPPORTED), (dict(T=2 ** 31), UNSUPPORTED),
     (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID), (dict(log_decay=0), INVALID), (dict(o=0), INVALID),
     (dict(q=P(0) + 4), MISALIGNED), (dict(lengths=P(4) + 4), MISALIGNED), (dict(s_in=P(5) + 8), MISALIGNED),
     (dict(s_out=P(7) + 4), MISALIGNED), (dict(o=P(6) + 2), MISALIGNED),
@@ -105,6 +105,7 @@ def bwd(B=2, T=9, H=2, K=64, V=64, dtype=1, grad=0, strides=None, ws=(0, 0), **p
 
 @pytest.mark.parametrize("kw,want", [
     (dict(H=0), INVALID), (dict(dtype=0, grad=1), UNSUPPORTED), (dict(K=12), UNSUPPORTED), (dict(V=256), UNSUPPORTED),
+    (dict(B=2 ** 21 + 1, H=1), UNSUPPORTED),    # 6 workgroups of 256 for each: 2^32 work-items are not launched
     (dict(d_o=0), INVALID), (dict(dq=0), INVALID), (dict(dk=0), INVALID), (dict(dv=0), INVALID),
     (dict(dv=P(10) + 4), MISALIGNED), (dict(ds_in=P(11) + 4), MISALIGNED),
     (dict(dk=P(8)), INVALID), (dict(dv=P(2)), INVALID), (dict(ds_in=P(5)), INVALID), (dict(ds_in=P(7) + 64), INVALID),
