@@ -11,7 +11,9 @@ Calls on torch's current stream take their workspace from torch's allocator
 captured in a HIP graph (``torch.cuda.graph``).  Calls with a ``stream`` of
 their own take it from the library's pool; to be recorded there they are given
 a ``workspace``, a uint8 tensor of at least ``fwd_workspace_bytes`` /
-``bwd_workspace_bytes`` bytes.
+``bwd_workspace_bytes`` bytes.  New outputs always come from torch's allocator
+on its current stream: with a ``stream`` of their own, callers order the two
+streams.
 """
 from __future__ import annotations
 
@@ -322,12 +324,23 @@ def rope(q, k, freqs, positions=None, start: int = 0, layout: str = "half", inve
     return q_out, k_out
 
 
+def _turned(q, k, freqs, positions, start, layout, stream):
+    """Turned copies of q and k that live for one call on `stream`: torch's
+    allocator must not hand them out on its own stream before that has run."""
+    q, k = rope(q, k, freqs, positions, start, layout, stream=stream)
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), q.device)
+        q.record_stream(s)
+        k.record_stream(s)
+    return q, k
+
+
 def retention(q, k, v, log_decay, freqs, positions=None, start: int = 0, layout: str = "half", **fwd_arguments):
     """fwd of q and k turned by their positions: a state whose decay is complex,
     exp(log_decay[h] + i freqs).  Returns (o, s_out) of fwd, whose other
     arguments it takes; s_in and s_out are states of turned keys, so a next
     piece of the sequence goes on with the next positions."""
-    q, k = rope(q, k, freqs, positions, start, layout, stream=fwd_arguments.get("stream"))
+    q, k = _turned(q, k, freqs, positions, start, layout, fwd_arguments.get("stream"))
     return fwd(q, k, v, log_decay, **fwd_arguments)
 
 
@@ -336,7 +349,7 @@ def retention_bwd(q, k, v, log_decay, do, freqs, positions=None, start: int = 0,
     """Gradients of retention(...): those of bwd at the turned q and k, turned
     back.  Other arguments as bwd."""
     stream = bwd_arguments.get("stream")
-    q, k = rope(q, k, freqs, positions, start, layout, stream=stream)
+    q, k = _turned(q, k, freqs, positions, start, layout, stream)
     g = bwd(q, k, v, log_decay, do, **bwd_arguments)
     rope(g["q"], g["k"], freqs, positions, start, layout, inverse=True, q_out=g["q"], k_out=g["k"], stream=stream)
     return g

@@ -119,6 +119,27 @@ def test_training_pass(linattn):
         assert abs(slope - want) <= 3e-6 * size
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_turned_copies_outlive_the_call(linattn, handle):
+    """On a stream of the caller's, behind other work: memory that the call has
+    given back is not written by torch's own stream before it has run."""
+    g = generator(6)
+    q, k, v, do = (normal(g, B, 200, H, D, dtype=torch.bfloat16).cuda() for _ in range(4))
+    freqs, decay = linattn.rope_freqs(D), DECAY.cuda()
+    want, _ = linattn.retention(q, k, v, decay, freqs)
+    grads = linattn.retention_bwd(q, k, v, decay, do, freqs)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    stream = side.cuda_stream if handle else side
+    got, _ = linattn.retention(q, k, v, decay, freqs, stream=stream)
+    got_grads = linattn.retention_bwd(q, k, v, decay, do, freqs, stream=stream)
+    spoiled = [torch.full_like(q, float("nan")) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert bits(got, want) and all(bits(got_grads[n], grads[n]) for n in grads) and spoiled
+
+
 def test_decode_step_as_a_graph(linattn, weights):
     """One captured step whose state is updated in place, replayed for token after token."""
     freqs = linattn.rope_freqs(D)
