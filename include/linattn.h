@@ -179,7 +179,7 @@ int linattn_rms_norm(int64_t rows, int64_t C, const void* x, const void* residua
 
 /*
  * linattn_rms_norm_q8 -- the same with an 8-bit output: each group of columns
- * has the scale max|y| / 448 (1 where every y is 0), and
+ * has the scale max|y| / 448 (at least 2^-126; 1 where every y is 0), and
  *
  *     codes = y / scale, rounded to the nearest e4m3 value (OCP e4m3fn, ties
  *     to even)

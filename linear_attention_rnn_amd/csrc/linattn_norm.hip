@@ -20,6 +20,10 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 
+// The scale of values up to `top`.  At least the smallest normal float32: top /
+// 448 in fewer bits, or rounded to zero, would leave codes past 448.
+__device__ __forceinline__ float scale_of(float top) { return top > 0.f ? fmaxf(top / kE4m3Max, 0x1p-126f) : 1.f; }
+
 template <bool BF>
 __device__ __forceinline__ void get8(const void* p, int64_t i, float (&x)[8]) {
   if constexpr (BF) {
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(Norm a) {
       if constexpr (OUT == 1) {
         // 16 lanes hold 128 adjacent columns
         top = over_lanes<16, true>(top);
-        const float scale = top > 0.f ? top / kE4m3Max : 1.f;
+        const float scale = scale_of(top);
         if (c < a.C) {
           if ((at & 15) == 0) a.scales[row * ((a.C + 127) / 128) + c / 128] = scale;
 #pragma unroll
@@ -198,7 +202,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(Norm a) {
   }
   if constexpr (OUT == 2) {
     top = over_row<TPR, true>(top, lds[1]);
-    const float scale = top > 0.f ? top / kE4m3Max : 1.f;
+    const float scale = scale_of(top);
     if (at == 0) a.scales[row] = scale;
 #pragma unroll
     for (int v = 0; v < NV; ++v)

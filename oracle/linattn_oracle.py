@@ -112,9 +112,9 @@ def e4m3_nearest(x):
 
 
 def scales_ref(y, group):
-    """Scales of 8-bit rows: max|y| / 448 over `group` columns (0: the row), 1 where all are 0."""
+    """Scales of 8-bit rows: max|y| / 448 over `group` columns (0: the row), at least 2^-126; 1 where all are 0."""
     y = np.asarray(y, np.float64)
     w = group or y.shape[-1]
     tops = [np.abs(y[..., c:c + w]).max(-1) for c in range(0, y.shape[-1], w)]
     s = np.stack(tops, -1) / 448.0
-    return np.where(s > 0, s, 1.0)
+    return np.where(s > 0, np.maximum(s, 2.0 ** -126), 1.0)

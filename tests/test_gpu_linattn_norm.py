@@ -133,6 +133,27 @@ def test_extremes(linattn):
     assert torch.all(y[5] == 0) and torch.all(codes.float()[5] == 0) and torch.all(scales[5] == 1)
 
 
+@pytest.mark.parametrize("group", [0, 128])
+def test_tiny_outputs(linattn, group):
+    """Outputs below the normal float32 range: scales stay normal, codes finite.
+
+    y errs by 30 U of itself and by two steps of 2^-149 (the products that
+    leave the normal range), the code by half a step: 2^-4 of it, or 2^-10."""
+    x = normal(generator(2), 3, 384, std=1.0)
+    w = torch.tensor([1e-42, 3e-45, 2e-37]).repeat_interleave(128)
+    if not group:
+        w = w.clamp(max=1e-42)
+    codes, scales, _ = linattn.rms_norm_q8(x.cuda(), w.cuda(), 1e-5, group=group)
+    y = R.rms_norm_ref(f64(x), f64(w), 1e-5)
+    s = R.scales_ref(y, group)
+    unit = 2.0 ** -126
+    within("scales", np.abs(f64(scales) - s) / unit, 32 * U * s / unit)
+    s = np.repeat(s, group or 384, -1)
+    got = f64(codes) * s
+    assert np.isfinite(got).all()
+    within("values", np.abs(got - y) / unit, (2.0 ** -4 * np.abs(y) + 2.0 ** -10 * s + 2.0 ** -148) / unit)
+
+
 def test_shapes_and_empty(linattn):
     x = normal(generator(2), 3, 5, 64, dtype=torch.bfloat16).cuda()
     w = torch.ones(64, device="cuda")
