@@ -142,7 +142,7 @@ size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
  *   B, T, H, D, R   batch, tokens, heads, channels of a head (a multiple of 8
  *             up to LINATTN_MAX_HEAD) and rotated channels (even, from 2 to
  *             D); channels from R on are copied.  Fastest where R (half
- *             layout: R / 2) is a multiple of 8.
+ *             layout: R / 2) is a multiple of 8.  B * T is at most 2^27, H 2^20.
  *   q, k      [B, T, H, D] of `dtype`; k may be NULL (q alone is turned)
  *   q_out, k_out   the same shape and type; q_out may be q itself and k_out k
  *             itself (with the same strides), in place.
@@ -168,7 +168,8 @@ int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const vo
  * with the mean over the C columns of each row.  The norm is that of h as it
  * is stored, so that linattn_rms_norm_bwd sees the same values.
  *
- *   rows, C   C is a multiple of 8 up to LINATTN_MAX_COLUMNS
+ *   rows, C   C is a multiple of 8 up to LINATTN_MAX_COLUMNS; at most 2^25
+ *             rows, or 2^22 of more than 2048 columns
  *   x, residual, h, y   [rows, C] of `dtype`, contiguous.  residual and h are
  *             both NULL (h = x) or both given; h may be x or residual itself.
  *   weight    C float32 values

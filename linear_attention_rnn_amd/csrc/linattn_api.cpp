@@ -113,6 +113,10 @@ int check_overlaps(const Span* s, int n, const int (*allowed)[2], int na) {
   return WKV6_OK;
 }
 
+// What a C entry returns where the host's memory gives out (an error text, the
+// list of pools): no exception leaves it.
+int no_memory() { return WKV6_ERR_HIP; }
+
 int present(const char* name, const void* p) {
   if (!p) return invalid(std::string("null pointer: ") + name);
   if (reinterpret_cast<uintptr_t>(p) % 16)
@@ -267,7 +271,10 @@ int norm_sizes(int64_t rows, int64_t C, float eps, int dtype) {
   if (st != WKV6_OK) return st;
   if (!(std::isfinite(eps) && eps >= 0.f)) return invalid("eps must be finite and >= 0");
   if (C % 8 || C > LINATTN_MAX_COLUMNS) return unsupported("C must be a multiple of 8 up to 16384");
-  if (rows > (1 << 22)) return unsupported("rows exceed the supported number (2^22)");
+  // a launch holds fewer than 2^32 work-items: 64 for each of many rows of up
+  // to 2048 columns, else up to 512
+  if (rows > (C <= 2048 ? 1 << 25 : 1 << 22))
+    return unsupported("rows exceed the supported number (2^25, or 2^22 of more than 2048 columns)");
   return WKV6_OK;
 }
 
@@ -278,19 +285,21 @@ extern "C" {
 int linattn_abi_version(void) { return LINATTN_ABI_VERSION; }
 
 size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, int dtype, int out_dtype,
-                                   int state_out) {
+                                   int state_out) try {
   set_error(WKV6_OK, "");
   if (check_sizes(B, T, H, K, V, dtype, out_dtype) != WKV6_OK || B == 0 || T == 0) return 0;
   linattn::Sweep a = base_sweep(B, T, H, K, V, nullptr, nullptr, dtype, out_dtype);
   float any = 0.f;
   a.s_out = state_out ? &any : nullptr;
   return linattn::sweep_workspace_bytes(&a, 1);
+} catch (...) {
+  return 0;
 }
 
 int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const void* q, const void* k, const void* v,
                 const float* log_decay, float scale, const int32_t* lengths, const float* s_in, void* o, float* s_out,
                 const int64_t* strides, int dtype, int out_dtype, void* workspace, size_t workspace_bytes,
-                void* stream) {
+                void* stream) try {
   set_error(WKV6_OK, "");
   int st = check_sizes(B, T, H, K, V, dtype, out_dtype);
   if (st != WKV6_OK || B == 0) return st;
@@ -323,10 +332,12 @@ int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   Workspace ws(hs);
   if ((st = ws.take(workspace, workspace_bytes, linattn::sweep_workspace_bytes(&a, 1))) != WKV6_OK) return st;
   return ws.done(linattn::enqueue_sweeps(&a, 1, ws.p, hs));
+} catch (...) {
+  return no_memory();
 }
 
 size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, int dtype, int grad_dtype,
-                                   int state_grad) {
+                                   int state_grad) try {
   set_error(WKV6_OK, "");
   if (check_sizes(B, T, H, K, V, dtype, grad_dtype) != WKV6_OK || B == 0 || T == 0) return 0;
   const Tensor none[7] = {};
@@ -334,12 +345,14 @@ size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
   float any = 0.f;
   bwd_sweeps(B, T, H, K, V, nullptr, 1.f, nullptr, nullptr, nullptr, state_grad ? &any : nullptr, none, dtype, grad_dtype, w);
   return linattn::sweep_workspace_bytes(w, 3);
+} catch (...) {
+  return 0;
 }
 
 int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const void* q, const void* k, const void* v,
                 const float* log_decay, float scale, const int32_t* lengths, const float* s_in, const void* d_o,
                 const float* ds_out, void* dq, void* dk, void* dv, float* ds_in, const int64_t* strides, int dtype,
-                int grad_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+                int grad_dtype, void* workspace, size_t workspace_bytes, void* stream) try {
   set_error(WKV6_OK, "");
   int st = check_sizes(B, T, H, K, V, dtype, grad_dtype);
   if (st != WKV6_OK || B == 0) return st;
@@ -376,11 +389,13 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   Workspace ws(hs);
   if ((st = ws.take(workspace, workspace_bytes, linattn::sweep_workspace_bytes(w, 3))) != WKV6_OK) return st;
   return ws.done(linattn::enqueue_sweeps(w, 3, ws.p, hs));
+} catch (...) {
+  return no_memory();
 }
 
 int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const void* q, const void* k, void* q_out,
                  void* k_out, const int32_t* positions, int64_t start, const double* freqs, int layout, int inverse,
-                 const int64_t* strides, int dtype, void* stream) {
+                 const int64_t* strides, int dtype, void* stream) try {
   set_error(WKV6_OK, "");
   if (B < 0 || T < 0 || H < 1) return invalid("sizes must be B, T >= 0 and H >= 1");
   int st = known_dtype(dtype);
@@ -424,6 +439,8 @@ int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const vo
   a.inverse = inverse != 0;
   a.bf16 = dtype == WKV6_DTYPE_BF16;
   return finished(linattn::enqueue_rope(a, static_cast<hipStream_t>(stream)));
+} catch (...) {
+  return no_memory();
 }
 
 }  // extern "C"
@@ -478,29 +495,35 @@ linattn::NormBwd norm_bwd_args(int64_t rows, int64_t C, int dtype) {
 extern "C" {
 
 int linattn_rms_norm(int64_t rows, int64_t C, const void* x, const void* residual, const float* weight, float eps,
-                     void* h, void* y, int dtype, void* stream) {
+                     void* h, void* y, int dtype, void* stream) try {
   set_error(WKV6_OK, "");
   if (rows > 0 && !y) return invalid("null pointer: y");
   return norm_call(rows, C, x, residual, weight, eps, h, y, nullptr, nullptr, 0, dtype, stream);
+} catch (...) {
+  return no_memory();
 }
 
 int linattn_rms_norm_q8(int64_t rows, int64_t C, const void* x, const void* residual, const float* weight, float eps,
-                        void* h, void* codes, float* scales, int group, int dtype, void* stream) {
+                        void* h, void* codes, float* scales, int group, int dtype, void* stream) try {
   set_error(WKV6_OK, "");
   if (group != 0 && group != 128) return invalid("group must be 0 or 128");
   return norm_call(rows, C, x, residual, weight, eps, h, nullptr, static_cast<uint8_t*>(codes), scales, group, dtype,
                    stream);
+} catch (...) {
+  return no_memory();
 }
 
-size_t linattn_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t C, int dtype) {
+size_t linattn_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t C, int dtype) try {
   set_error(WKV6_OK, "");
   if (norm_sizes(rows, C, 0.f, dtype) != WKV6_OK) return 0;
   return linattn::norm_bwd_workspace_bytes(norm_bwd_args(rows, C, dtype));
+} catch (...) {
+  return 0;
 }
 
 int linattn_rms_norm_bwd(int64_t rows, int64_t C, const void* dy, const void* h, const void* dh, const float* weight,
                          float eps, void* dx, float* dweight, int dtype, void* workspace, size_t workspace_bytes,
-                         void* stream) {
+                         void* stream) try {
   set_error(WKV6_OK, "");
   int st = norm_sizes(rows, C, eps, dtype);
   if (st != WKV6_OK) return st;
@@ -527,6 +550,8 @@ int linattn_rms_norm_bwd(int64_t rows, int64_t C, const void* dy, const void* h,
   Workspace ws(static_cast<hipStream_t>(stream));
   if ((st = ws.take(workspace, workspace_bytes, linattn::norm_bwd_workspace_bytes(a))) != WKV6_OK) return st;
   return ws.done(linattn::enqueue_norm_bwd(a, ws.p, ws.stream));
+} catch (...) {
+  return no_memory();
 }
 
 }  // extern "C"

@@ -154,6 +154,21 @@ def test_tiny_outputs(linattn, group):
     within("values", np.abs(got - y) / unit, (2.0 ** -4 * np.abs(y) + 2.0 ** -10 * s + 2.0 ** -148) / unit)
 
 
+def test_many_rows(linattn):
+    """More rows than 2^22, as norms over the channels of a head have: both ends and one in the middle."""
+    rows = 2 ** 22 + 5
+    x = normal(generator(3), 64, 64, std=1.0, dtype=torch.bfloat16).cuda()
+    big = x.repeat(rows // 64 + 1, 1)[:rows]
+    w = torch.ones(64, device="cuda")
+    y, _ = linattn.rms_norm(big, w)
+    want, _ = linattn.rms_norm(x.repeat(40, 1), w)   # the same shape of workgroups
+    for at in (0, 2 ** 21, 2 ** 22 - 64, rows - rows % 64):
+        n = min(64, rows - at)
+        assert bits(y[at:at + n], want[:n])
+    g = linattn.rms_norm_bwd(big, big, w)
+    assert torch.isfinite(g["weight"]).all() and bits(g["x"][:64], g["x"][2 ** 22 - 64:2 ** 22])
+
+
 def test_shapes_and_empty(linattn):
     x = normal(generator(2), 3, 5, 64, dtype=torch.bfloat16).cuda()
     w = torch.ones(64, device="cuda")
