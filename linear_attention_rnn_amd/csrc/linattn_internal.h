@@ -58,7 +58,7 @@ struct SweepPlan {
   Sweep a[kSweeps];
   int sweeps;
   bool state_out;   // the call hands back a state
-  float* ws;        // [sweeps][B H][segments] entering states; null for one segment
+  float* ws;        // [sweeps][B H][segments] states of segments; null for one segment
   int segments;     // of each sequence
   int seg_tokens;   // tokens of a segment, a multiple of 64
   int vblocks;      // blocks of 64 value channels, the most of the sweeps

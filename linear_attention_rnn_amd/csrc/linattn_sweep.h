@@ -159,6 +159,19 @@ __device__ __forceinline__ int64_t segment_state(const SweepPlan& p, int sweep, 
   return ((sweep * p.pairs + pair) * p.segments + seg) * (KP * kVBlock * p.vblocks);
 }
 
+// Tokens of segment s of a sequence of `len`.
+__device__ __forceinline__ float tokens_in(const SweepPlan& p, int64_t len, int s) {
+  const int64_t left = len - (int64_t)s * p.seg_tokens;
+  return (float)(left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens);
+}
+
+// Up to so many segments, each adds up the earlier ones' states by itself;
+// more get theirs from the carry kernel.  Measured, us, so and with the kernel:
+// 4 segments (float32, 6 x 1023 tokens, V = 96) 59.7 / 64.0, 3 (float32
+// gradients, K = 128) 64.8 / 67.9; 16 (8192 tokens of 16 heads of 128 x 128)
+// 79.8 / 73.7, 128 40.3 / 31.0.
+constexpr int kJoin = 8;
+
 template <int KP, bool BF, int MP>
 constexpr int occupancy() {
   return KP == 64 ? (BF && MP == 1 ? 3 : 2) : (BF ? 2 : 1);
@@ -205,16 +218,12 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
     const int c = 32 * J + 8 * g + 4 * e + r;
     return c < a.K && sn < a.V ? (c * cs + sn * ns) * 4 : wkv6::kOffNone;
   };
-  float* const seg_state = p.ws ? p.ws + segment_state<KP>(p, sweep, pair, seg) + ((vb * 4 + w) * NJ * 2 * 64 + lane) * 4 : nullptr;
-  if constexpr (SUMMARY) {
-#pragma unroll
-    for (int J = 0; J < NJ; ++J) M[J][0] = M[J][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  } else if (seg_state) {
-#pragma unroll
-    for (int J = 0; J < NJ; ++J)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) M[J][e] = *reinterpret_cast<const f32x4*>(seg_state + (2 * J + e) * 256);
-  } else {
+  // Workspace, per segment: first its own state, which the carry kernel turns
+  // into the entering one; the last place holds s_in, for s_out may be s_in.
+  const auto place = [&](int s) {
+    return reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, sweep, pair, s)) + (vb * 4 + w) * NJ * 2 * 64 + lane;
+  };
+  const auto read_in = [&](f32x4 (&m)[NJ][2]) {
     // (unconditional buffer loads: a branch around each would wait for each)
     const float* s_from = a.s_in ? a.s_in + pair * KV : nullptr;
     const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s_from), (short)0, s_from ? KV * 4 : 0, wkv6::kRsrcFlags);
@@ -224,7 +233,31 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          M[J][e][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(J, e, r), 0, 0));
+          m[J][e][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(J, e, r), 0, 0));
+  };
+  const auto write = [&](f32x4* to, const f32x4 (&m)[NJ][2]) {
+#pragma unroll
+    for (int i = 0; i < 2 * NJ; ++i) to[64 * i] = m[i / 2][i % 2];
+  };
+  f32x4 Sin[SUMMARY ? NJ : 1][2];
+  if constexpr (SUMMARY) {
+    if (seg == 0) read_in(Sin);
+#pragma unroll
+    for (int J = 0; J < NJ; ++J) M[J][0] = M[J][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else if (!p.ws) {
+    read_in(M);
+  } else {
+    const bool join = p.segments <= kJoin;
+    const f32x4* from = place(join ? p.segments - 1 : seg);
+#pragma unroll
+    for (int i = 0; i < 2 * NJ; ++i) M[i / 2][i % 2] = from[64 * i];
+    if (join)
+      for (int s = 0; s < seg; ++s) {
+        const float d = ex2(gl * tokens_in(p, len, s));
+        from = place(s);
+#pragma unroll
+        for (int i = 0; i < 2 * NJ; ++i) M[i / 2][i % 2] = M[i / 2][i % 2] * d + from[64 * i];
+      }
   }
 
   // ---- factors of whole chunks
@@ -426,10 +459,8 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
 
   // ---- hand on the state
   if constexpr (SUMMARY) {
-#pragma unroll
-    for (int J = 0; J < NJ; ++J)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4*>(seg_state + (2 * J + e) * 256) = M[J][e];
+    write(place(seg), M);
+    if (seg == 0) write(place(p.segments - 1), Sin);
   } else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
     const Rsrc rt = __builtin_amdgcn_make_buffer_rsrc(a.s_out + pair * KV, (short)0, KV * 4, wkv6::kRsrcFlags);
 #pragma unroll
@@ -462,22 +493,11 @@ constexpr int kCarryThreads = 128;
 template <int KP>
 __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
   const Sweep& a = p.a[blockIdx.z];
-  const int64_t pair = blockIdx.x;
-  const int i4 = blockIdx.y * kCarryThreads + threadIdx.x, size = KP * kVBlock * p.vblocks;   // 4 adjacent of `size` elements
+  const int64_t pair = blockIdx.x, next = KP * kVBlock * p.vblocks / 4;
   const int64_t len = tokens_of(a, pair / a.H);
   const float gl = log2_decay(a.log_decay[pair % a.H]);
-  f32x4 m = {0.f, 0.f, 0.f, 0.f};
-  if (a.s_in) {
-    const int lane = i4 & 63, g = lane >> 4, li = lane & 15, t = i4 >> 6;
-    const int e = t & 1, J = t / 2 % (KP / 32), w = t / (KP / 16) & 3, vb = t / (KP / 4);
-    const int c = 32 * J + 8 * g + 4 * e, n = vb * kVBlock + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
-    const float* s = a.s_in + pair * a.K * a.V + (a.s_transposed ? n * a.K + c : c * a.V + n);
-    if (c < a.K && n < a.V)   // K is a multiple of 8
-#pragma unroll
-      for (int r = 0; r < 4; ++r) m[r] = s[a.s_transposed ? r : r * a.V];
-  }
-  f32x4* at = reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, blockIdx.z, pair, 0)) + i4;
-  const int64_t next = size / 4;
+  f32x4* at = reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, blockIdx.z, pair, 0)) + blockIdx.y * kCarryThreads + threadIdx.x;
+  f32x4 m = at[(p.segments - 1) * next];
   for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
     f32x4 u[kAhead];   // loaded together: the chain through m must not wait for memory
 #pragma unroll
@@ -488,9 +508,7 @@ __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
       const int s = s0 + i;
       if (s >= p.segments) break;
       at[s * next] = m;
-      const int64_t left = len - (int64_t)s * p.seg_tokens;
-      const int64_t n = left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens;
-      if (s + 1 < p.segments) m = m * ex2(gl * (float)n) + u[i];
+      if (s + 1 < p.segments) m = m * ex2(gl * tokens_in(p, len, s)) + u[i];
     }
   }
 }
@@ -503,7 +521,7 @@ hipError_t launch(const SweepPlan& p, hipStream_t s) {
     q.items = p.pairs * (p.segments - 1);
     const unsigned parts = (unsigned)(KP * kVBlock * p.vblocks / (4 * kCarryThreads));
     hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, true>), grid(q.items), dim3(NTH), 0, s, q);
-    hipLaunchKernelGGL(carry_kernel<KP>, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(kCarryThreads), 0, s, p);
+    if (p.segments > kJoin) hipLaunchKernelGGL(carry_kernel<KP>, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(kCarryThreads), 0, s, p);
   }
   hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, false>), grid(p.items), dim3(NTH), 0, s, p);
   return hipGetLastError();
