@@ -11,10 +11,10 @@
 //
 // All exponents are >= 0, so every factor is at most 1 for a decay a <= 1.
 //
-// A workgroup of four waves runs one (batch item, head, block of 64 value
-// channels, segment).  Wave w computes the outputs of tokens 16w..16w+15 (all
-// 64 channels, transposed: O^T[n][t]) and keeps the state's columns of its
-// strip of 16 value channels in registers.  MFMA operands chain without a
+// A workgroup of four waves (eight: see waves()) runs one (batch item, head,
+// block of 64 value channels, segment).  Wave w computes the outputs of tokens
+// 16w..16w+15 (all 64 channels, transposed: O^T[n][t]) and keeps the state's
+// columns of its strip of 16 value channels in registers.  MFMA operands chain without a
 // detour: scores come out as K Q^T tiles whose accumulator lanes are, tile
 // pairs taken together, the operand lanes of the product with V^T; the state's
 // accumulators are the operand lanes of the product with q.  Only the state
@@ -174,16 +174,30 @@ constexpr int kJoin = 8;
 
 template <int KP, bool BF, int MP>
 constexpr int occupancy() {
-  return KP == 64 ? (BF && MP == 1 ? 3 : 2) : (BF ? 2 : 1);
+  return KP == 64 ? (BF && MP == 1 ? 3 : 2) : 2;
+}
+
+// Waves of a workgroup.  LDS holds one float32 workgroup of more than 64 key
+// channels at a time, so that one gets a second set of waves: the outputs'
+// value channels and the state's key channels are shared out between the two
+// (gradients of K = 128, V = 64, 2 x 777 tokens: 64.6 -> 61.6 us; prompts of
+// 128 x 128: 100.5 -> 95.4).  With K = 64 two workgroups fit, and eight waves
+// of one are slower (60 -> 74 us).
+template <int KP, bool BF>
+constexpr int waves() {
+  return KP == 128 && !BF ? 8 : 4;
 }
 
 template <int KP, bool BF, int MP, int UP, bool OBF, bool SUMMARY>
-__global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
+__global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
+  constexpr int NW = waves<KP, BF>(), NT = 64 * NW, PARTS = NW / 4;
   constexpr int NI = BF ? 1 : 3;             // parts of an input operand
   constexpr int ISZ = BF ? 2 : 4;
   constexpr int NJ = KP / 32;                // groups of 32 key channels
   constexpr int KPL = (KP / 64) * kPlane;    // one part of the keys
-  constexpr int KR = KP / 32;                // key chunks of 8 channels a thread loads
+  constexpr int KR = KP * 8 / NT;            // key chunks of 8 channels a thread loads
+  constexpr int VR = 512 / NT;
+  constexpr int MJ = NJ / PARTS, OU = 2 / PARTS;
   __shared__ __bf16 Kp[NI * KPL];
   __shared__ __bf16 Vp[NI * kPlane];
   __shared__ __bf16 Sp[SUMMARY ? 8 : MP * KP * 64];
@@ -201,7 +215,9 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   const int seg = (int)(item % segs);
   const int64_t b = pair / a.H, h = pair % a.H;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int part = wave >> 2, w = wave & 3;        // of the state: strip w, its key groups MJ * part..
+  const int tb = part ? 3 - w : w;                 // of the outputs: tokens 16 tb.., values 32 OU part..
   const float gl = log2_decay(a.log_decay[h]);
 
   const int64_t len = tokens_of(a, b);
@@ -210,58 +226,58 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   const int nch = lo < hi ? (int)((hi - lo + kChunk - 1) / kChunk) : 0;
 
   // ---- the entering state: rows c = 32J + 8g + 4e + r, column n of strip w
-  f32x4 M[NJ][2];
+  f32x4 M[MJ][2];
   const int sn = v0 + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
   const int KV = a.K * a.V;
   const int cs = a.s_transposed ? 1 : a.V, ns = a.s_transposed ? a.K : 1;
   const auto state_offset = [&](int J, int e, int r) {
-    const int c = 32 * J + 8 * g + 4 * e + r;
+    const int c = 32 * (MJ * part + J) + 8 * g + 4 * e + r;
     return c < a.K && sn < a.V ? (c * cs + sn * ns) * 4 : wkv6::kOffNone;
   };
   // Workspace, per segment: first its own state, which the carry kernel turns
   // into the entering one; the last place holds s_in, for s_out may be s_in.
   const auto place = [&](int s) {
-    return reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, sweep, pair, s)) + (vb * 4 + w) * NJ * 2 * 64 + lane;
+    return reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, sweep, pair, s)) + ((vb * 4 + w) * NJ + MJ * part) * 2 * 64 + lane;
   };
-  const auto read_in = [&](f32x4 (&m)[NJ][2]) {
+  const auto read_in = [&](f32x4 (&m)[MJ][2]) {
     // (unconditional buffer loads: a branch around each would wait for each)
     const float* s_from = a.s_in ? a.s_in + pair * KV : nullptr;
     const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s_from), (short)0, s_from ? KV * 4 : 0, wkv6::kRsrcFlags);
 #pragma unroll
-    for (int J = 0; J < NJ; ++J)
+    for (int J = 0; J < MJ; ++J)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           m[J][e][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(J, e, r), 0, 0));
   };
-  const auto write = [&](f32x4* to, const f32x4 (&m)[NJ][2]) {
+  const auto write = [&](f32x4* to, const f32x4 (&m)[MJ][2]) {
 #pragma unroll
-    for (int i = 0; i < 2 * NJ; ++i) to[64 * i] = m[i / 2][i % 2];
+    for (int i = 0; i < 2 * MJ; ++i) to[64 * i] = m[i / 2][i % 2];
   };
-  f32x4 Sin[SUMMARY ? NJ : 1][2];
+  f32x4 Sin[SUMMARY ? MJ : 1][2];
   if constexpr (SUMMARY) {
     if (seg == 0) read_in(Sin);
 #pragma unroll
-    for (int J = 0; J < NJ; ++J) M[J][0] = M[J][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int J = 0; J < MJ; ++J) M[J][0] = M[J][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   } else if (!p.ws) {
     read_in(M);
   } else {
     const bool join = p.segments <= kJoin;
     const f32x4* from = place(join ? p.segments - 1 : seg);
 #pragma unroll
-    for (int i = 0; i < 2 * NJ; ++i) M[i / 2][i % 2] = from[64 * i];
+    for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = from[64 * i];
     if (join)
       for (int s = 0; s < seg; ++s) {
         const float d = ex2(gl * tokens_in(p, len, s));
         from = place(s);
 #pragma unroll
-        for (int i = 0; i < 2 * NJ; ++i) M[i / 2][i % 2] = M[i / 2][i % 2] * d + from[64 * i];
+        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = M[i / 2][i % 2] * d + from[64 * i];
       }
   }
 
   // ---- factors of whole chunks
-  const float f_inter = ex2(gl * (16 * w + li + (rev ? 0 : 1))) * a.is;   // column t = 16w + li
+  const float f_inter = ex2(gl * (16 * tb + li + (rev ? 0 : 1))) * a.is;   // column t = 16tb + li
   float dg[4], of[4];   // tile of the wave's own tokens; the tile before it
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -283,37 +299,37 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   update_factors(kChunk);
 
   // ---- loads of a chunk of nt tokens (none: everything out of range)
-  Raw8<BF> kr[KR], vr[2], qr[SUMMARY ? 1 : NJ];
+  Raw8<BF> kr[KR], vr[VR], qr[SUMMARY ? 1 : NJ];
   Rows rk, rv, rq, ro;
-  int ok[KR], ov[2], oq[NJ] = {}, oo[2] = {};
+  int ok[KR], ov[VR], oq[NJ] = {}, oo[OU] = {};
   constexpr int OSZ = OBF ? 2 : 4;
   rk.start(a.k, b, h, lo, len, rev, ISZ);
   rv.start(a.v, b, h, lo, len, rev, ISZ);
 #pragma unroll
-  for (int x = 0; x < KR; ++x) ok[x] = rk.offset((tid + x * NTH) / (KP / 8), (tid + x * NTH) % (KP / 8) * 8, a.K, ISZ);
+  for (int x = 0; x < KR; ++x) ok[x] = rk.offset((tid + x * NT) / (KP / 8), (tid + x * NT) % (KP / 8) * 8, a.K, ISZ);
 #pragma unroll
-  for (int x = 0; x < 2; ++x) ov[x] = rv.offset((tid + x * NTH) / 8, v0 + tid % 8 * 8, a.V, ISZ);
+  for (int x = 0; x < VR; ++x) ov[x] = rv.offset((tid + x * NT) / 8, v0 + tid % 8 * 8, a.V, ISZ);
   if constexpr (!SUMMARY) {
     rq.start(a.q, b, h, lo, len, rev, ISZ);
     ro.start(a.o, b, h, lo, len, rev, OSZ);
 #pragma unroll
-    for (int J = 0; J < NJ; ++J) oq[J] = rq.offset(16 * w + li, 32 * J + 8 * g, a.K, ISZ);
+    for (int J = 0; J < NJ; ++J) oq[J] = rq.offset(16 * tb + li, 32 * J + 8 * g, a.K, ISZ);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) oo[u] = ro.offset(16 * w + li, v0 + 32 * u + 8 * g, a.V, OSZ);
+    for (int u = 0; u < OU; ++u) oo[u] = ro.offset(16 * tb + li, v0 + 32 * (OU * part + u) + 8 * g, a.V, OSZ);
   }
   const auto load = [&](int nt) {
     const Rsrc bk = rk.rsrc(), bv = rv.rsrc();
 #pragma unroll
-    for (int x = 0; x < KR; ++x) kr[x] = load8<BF>(bk, (tid + x * NTH) / (KP / 8) < nt ? ok[x] : wkv6::kOffNone);
+    for (int x = 0; x < KR; ++x) kr[x] = load8<BF>(bk, (tid + x * NT) / (KP / 8) < nt ? ok[x] : wkv6::kOffNone);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) vr[x] = load8<BF>(bv, (tid + x * NTH) / 8 < nt ? ov[x] : wkv6::kOffNone);
+    for (int x = 0; x < VR; ++x) vr[x] = load8<BF>(bv, (tid + x * NT) / 8 < nt ? ov[x] : wkv6::kOffNone);
     rk.at += rk.step;
     rv.at += rv.step;
     if constexpr (!SUMMARY) {
       const Rsrc bq = rq.rsrc();
 #pragma unroll
       for (int J = 0; J < NJ; ++J)
-        qr[J] = load8<BF>(bq, 16 * w + li < nt ? oq[J] : wkv6::kOffNone);
+        qr[J] = load8<BF>(bq, 16 * tb + li < nt ? oq[J] : wkv6::kOffNone);
       rq.at += rq.step;
     }
   };
@@ -329,26 +345,27 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
     // ---- keys, values and the state to LDS
 #pragma unroll
     for (int x = 0; x < KR; ++x) {
-      const int id = tid + x * NTH, row = id / (KP / 8), c8 = id % (KP / 8);
+      const int id = tid + x * NT, row = id / (KP / 8), c8 = id % (KP / 8);
       stage8<BF>(Kp + (c8 >> 3) * kPlane, KPL, swz(row, (c8 & 7) * 8), kr[x]);
     }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int id = tid + x * NTH;
+    for (int x = 0; x < VR; ++x) {
+      const int id = tid + x * NT;
       stage8<BF>(Vp, kPlane, swz(id / 8, id % 8 * 8), vr[x]);
     }
     Op<NI> qf[NJ];
     if constexpr (!SUMMARY) {
 #pragma unroll
-      for (int J = 0; J < NJ; ++J) {
-        qf[J] = operand<BF>(qr[J]);
+      for (int J = 0; J < NJ; ++J) qf[J] = operand<BF>(qr[J]);
+#pragma unroll
+      for (int J = 0; J < MJ; ++J) {
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = M[J][e >> 2][e & 3];
         const Op<MP> o = wkv6::split8<MP>(f);
 #pragma unroll
         for (int s = 0; s < MP; ++s)
-          *reinterpret_cast<bf16x8*>(Sp + ((s * 4 + w) * NJ + J) * 512 + lane * 8) = o.p[s];
+          *reinterpret_cast<bf16x8*>(Sp + ((s * 4 + w) * NJ + MJ * part + J) * 512 + lane * 8) = o.p[s];
       }
     }
     lds_barrier();
@@ -358,39 +375,39 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
     if constexpr (!SUMMARY) {
       {
         // ---- the state's part: O^T[n][t] = sum_c M[c][n] q_t[c]
-        f32x4 acc[4];
+        f32x4 acc[2 * OU];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < 2 * OU; ++s) {
           acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int J = 0; J < NJ; ++J)
-            acc[s] = mma<MP, NI>(read8<MP>(Sp, 4 * NJ * 512, (s * NJ + J) * 512 + lane * 8), qf[J], acc[s]);
+            acc[s] = mma<MP, NI>(read8<MP>(Sp, 4 * NJ * 512, ((2 * OU * part + s) * NJ + J) * 512 + lane * 8), qf[J], acc[s]);
           acc[s] *= f_inter;
         }
         // ---- the chunk's own part, two tiles of 16 tokens i at a time
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (2 * u <= w) {
+          if (2 * u <= tb) {
             float pr[8];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int I = 2 * u + e;
               f32x4 sc = {0.f, 0.f, 0.f, 0.f};
-              if (I <= w) {
+              if (I <= tb) {
 #pragma unroll
                 for (int J = 0; J < NJ; ++J)
                   sc = mma<NI, NI>(read8<NI>(Kp + (J >> 1) * kPlane, KPL, swz(16 * I + li, 32 * (J & 1) + 8 * g)), qf[J], sc);
-                const float far = I + 2 == w ? a16 : I + 3 == w ? a16 * a16 : 1.f;
+                const float far = I + 2 == tb ? a16 : I + 3 == tb ? a16 * a16 : 1.f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sc[r] *= I == w ? dg[r] : of[r] * far;
+                for (int r = 0; r < 4; ++r) sc[r] *= I == tb ? dg[r] : of[r] * far;
               }
 #pragma unroll
               for (int r = 0; r < 4; ++r) pr[4 * e + r] = sc[r];
             }
             const Op<MP> pf = wkv6::split8<MP>(pr);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const int row = 32 * u + 4 * g + (li >> 2), col = 4 * (s >> 1) + (li & 3);
+            for (int s = 0; s < 2 * OU; ++s) {
+              const int row = 32 * u + 4 * g + (li >> 2), col = 4 * (OU * part + (s >> 1)) + (li & 3);
               const Op<NI> vf = read_tr<NI>(Vp, kPlane, row * 64 + ((col ^ (row & 7)) << 3) + 4 * (s & 1),
                                             (row + 16) * 64 + ((col ^ (row & 7)) << 3) + 4 * (s & 1));
               acc[s] = mma<NI, MP>(vf, pf, acc[s]);
@@ -401,8 +418,8 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
         const Rsrc bo = ro.rsrc();
         ro.at += ro.step;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int off = 16 * w + li < nt ? oo[u] : wkv6::kOffNone;
+        for (int u = 0; u < OU; ++u) {
+          const int off = 16 * tb + li < nt ? oo[u] : wkv6::kOffNone;
           const f32x4 x = acc[2 * u], y = acc[2 * u + 1];
           if constexpr (OBF) {
             typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -424,7 +441,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
       if (nt < kChunk) update_factors(nt);
       const float an = ex2(gl * nt);
 #pragma unroll
-      for (int J = 0; J < NJ; ++J)
+      for (int J = 0; J < MJ; ++J)
 #pragma unroll
         for (int e = 0; e < 2; ++e) M[J][e] *= an;
 #pragma unroll
@@ -445,11 +462,11 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
           }
           const Op<UP> vf = wkv6::split8<UP>(f);
 #pragma unroll
-          for (int J = 0; J < NJ; ++J)
+          for (int J = 0; J < MJ; ++J)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int kc = 4 * (J & 1) + (li & 3);
-              M[J][e] = mma<NI, UP>(read_tr<NI>(Kp + (J >> 1) * kPlane, KPL, at_col(kc, e, 0), at_col(kc, e, 4)), vf, M[J][e]);
+              const int kj = MJ * part + J, kc = 4 * (kj & 1) + (li & 3);
+              M[J][e] = mma<NI, UP>(read_tr<NI>(Kp + (kj >> 1) * kPlane, KPL, at_col(kc, e, 0), at_col(kc, e, 4)), vf, M[J][e]);
             }
         }
       }
@@ -464,7 +481,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   } else if (a.s_out && ((last_seg && lo < hi) || (len == 0 && seg == 0))) {
     const Rsrc rt = __builtin_amdgcn_make_buffer_rsrc(a.s_out + pair * KV, (short)0, KV * 4, wkv6::kRsrcFlags);
 #pragma unroll
-    for (int J = 0; J < NJ; ++J)
+    for (int J = 0; J < MJ; ++J)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -475,7 +492,7 @@ __global__ __launch_bounds__(NTH, (occupancy<KP, BF, MP>())) void sweep_kernel(S
   // ---- rows behind the sequence: zero, each segment those of its own places
   if constexpr (!SUMMARY) {
     const int64_t z0 = len > lo ? len : lo, z1 = lo + p.seg_tokens < a.T ? lo + p.seg_tokens : a.T;
-    for (int64_t t = z0 + tid / 8; t < z1; t += NTH / 8) {
+    for (int64_t t = z0 + tid / 8; t < z1; t += NT / 8) {
       const int n = v0 + tid % 8 * 8;
       if (n < a.V) {
         char* q = static_cast<char*>(const_cast<void*>(a.o.p)) + (b * a.o.b + h * a.o.h + t * a.o.t + n) * OSZ;
@@ -520,10 +537,10 @@ hipError_t launch(const SweepPlan& p, hipStream_t s) {
     SweepPlan q = p;
     q.items = p.pairs * (p.segments - 1);
     const unsigned parts = (unsigned)(KP * kVBlock * p.vblocks / (4 * kCarryThreads));
-    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, true>), grid(q.items), dim3(NTH), 0, s, q);
+    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, true>), grid(q.items), dim3((64 * waves<KP, BF>())), 0, s, q);
     if (p.segments > kJoin) hipLaunchKernelGGL(carry_kernel<KP>, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(kCarryThreads), 0, s, p);
   }
-  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, false>), grid(p.items), dim3(NTH), 0, s, p);
+  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, false>), grid(p.items), dim3((64 * waves<KP, BF>())), 0, s, p);
   return hipGetLastError();
 }
 
