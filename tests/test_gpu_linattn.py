@@ -129,7 +129,7 @@ def test_layouts_do_not_matter(linattn, dtype, T):
     assert bits(guard[:, 1:-1], want) and torch.all(guard[:, 0] == 7) and torch.all(guard[:, -1] == 7)
 
 
-@pytest.mark.parametrize("T", [6, 70, 2100])
+@pytest.mark.parametrize("T", [6, 70, 2100, 2500])
 def test_state_in_place_and_pieces(linattn, T):
     """s_out may be s_in; a sequence in pieces equals the whole within the bounds; no token, no change."""
     x = inputs(T, 2, T, 2, 64, 64, "bf16")

@@ -102,7 +102,7 @@ def test_equals_differences_of_the_forward(linattn):  # noqa: F811
         assert abs(slope - want) <= 3e-6 * size
 
 
-@pytest.mark.parametrize("T", [7, 100, 1400])
+@pytest.mark.parametrize("T", [7, 100, 1400, 2500])
 def test_layouts_do_not_matter(linattn, T):  # noqa: F811
     """Inputs and gradients as slices of one buffer each; heads that share keys; states in place."""
     B, H, K = 2, 3, 64
