@@ -10,7 +10,10 @@
 namespace linattn {
 
 constexpr int kChunk = 64;       // tokens of a chunk
-constexpr int kStepTokens = 8;   // calls of at most so many tokens run token by token
+// Calls of at most so many tokens run token by token (us, so and in chunks: 2
+// tokens of 16 x 32 heads of 64 x 64 5.2 / 8.8, 8 tokens 8.6 / 9.0, 12 10.8 /
+// 9.0; of 12 heads 3.7 / 6.6, 6.6 / 6.7, 8.6 / 6.7).
+constexpr int kStepTokens = 8;
 constexpr int kVBlock = 64;      // value channels one workgroup handles
 
 // A [B, T, H, D] tensor: base and distances in elements (channels adjacent).

@@ -7,12 +7,12 @@
 namespace linattn {
 namespace {
 
-
 // A few tokens (decoding): the recurrence itself in float32,
 //   M <- a M + k_t^T v_t,   o_t = is q_t M,
 // with the state's 64 columns of a block in registers: thread (x, y) holds
 // rows y, y + 16, .. of columns 4x..4x+3.  Bound by the state's bytes, read
-// and written once as whole 256-byte rows.
+// and written once as whole 256-byte rows: one token of 256 x 32 heads of 64 x
+// 64, 50 us, 5.4 TB/s; of 12 heads 4 us, a launch.
 template <int KX, bool BF, bool OBF>
 __global__ __launch_bounds__(NTH) void step_kernel(Sweep a, int vblocks) {
   __shared__ float qk[2][kStepTokens][16 * KX];

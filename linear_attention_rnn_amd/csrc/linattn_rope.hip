@@ -4,7 +4,9 @@
 // Bound by the bytes of q and k, read and written once.  The angles of a
 // token are the same for all its heads, so a workgroup takes a few tokens,
 // puts the cosines and sines of their R / 2 angles into LDS and then streams
-// all heads of q and k past them, 16 bytes a load.
+// all heads of q and k past them, 16 bytes a load.  32768 tokens of 32 heads
+// of 64 channels in bfloat16: 92 us, 5.9 TB/s; one token of 64 sequences 3.6
+// us, a launch.
 //
 // Angles are products of whole positions and float64 frequencies, reduced to
 // a part of a turn before they are rounded to float32: the quotient by 2 pi is
@@ -21,8 +23,9 @@ namespace {
 
 constexpr int NTR = 256;
 constexpr int kMaxTokens = 16;     // of a workgroup
-constexpr int kMaxAngles = 1024;   // those times R / 2
-constexpr int kTogether = 4;       // tokens whose loads a thread has in flight
+constexpr int kMaxAngles = 1024;   // those times R / 2 <= 64
+constexpr int kTogether = 2;       // tokens whose loads a thread has in flight
+constexpr int kRows = 128;         // rows (tensor, token, head) of a workgroup
 
 __device__ __forceinline__ float2 turn_of(double angle, bool inverse) {
   constexpr double kInv2Pi = 0.15915494309189535;       // 1 / (2 pi), rounded
@@ -72,12 +75,12 @@ __device__ __forceinline__ void put(void* p, int64_t i, const float (&x)[N]) {
     __builtin_memcpy(__builtin_assume_aligned(at, N * Z > 16 ? 16 : N * Z), u, N * Z);
 }
 
-// blockIdx.x: a group of `tokens` tokens; blockIdx.y: a share of the rows
-// (tensor, head) of each token.  A piece is N adjacent channels: N / 2 pairs
+// blockIdx.x: a group of `tokens` tokens, whose rows (tensor, head) are worked
+// on kTogether tokens at a time.  A piece is N adjacent channels: N / 2 pairs
 // in place (interleaved), or N pairs whose halves lie R / 2 apart; N divides
 // what a piece must not cross (R, or R / 2).
 template <bool BF, bool INTER, int N>
-__global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens, int rows_share) {
+__global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens) {
   __shared__ float2 cs[kMaxAngles];
   __shared__ int64_t base[4][kMaxTokens];   // of a token's rows in q, k, q_out, k_out
   const int half = a.R / 2, tid = threadIdx.x;
@@ -98,11 +101,11 @@ __global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens, int rows_
   const int turning = INTER ? a.R / N : half / N, units = turning + (a.D - a.R) / N;
   const int per = NTR / units, u = tid % units, slot = tid / units;
   if (slot >= per) return;
-  const int all = a.k.p ? 2 * (int)a.H : (int)a.H, r0 = blockIdx.y * rows_share;
-  const int rows = all - r0 < rows_share ? all : r0 + rows_share;
+  const int rows = a.k.p ? 2 * (int)a.H : (int)a.H, items = rows * ((nt + kTogether - 1) / kTogether);
   const bool copy = u >= turning;
   const int c = copy ? a.R + N * (u - turning) : N * u;
-  for (int r = r0 + slot; r < rows; r += per) {
+  for (int item = slot; item < items; item += per) {
+    const int r = item % rows, t0 = item / rows * kTogether;
     const bool isk = r >= a.H;
     const Tensor& x = isk ? a.k : a.q;
     const Tensor& y = isk ? a.k_out : a.q_out;
@@ -110,41 +113,39 @@ __global__ __launch_bounds__(NTR) void rope_kernel(Rope a, int tokens, int rows_
     const int64_t* const fb = base[isk ? 1 : 0];
     const int64_t* const tb = base[isk ? 3 : 2];
     void* const out = const_cast<void*>(y.p);
-    // kTogether tokens at a time, all of their loads before the first store
-    for (int t0 = 0; t0 < nt; t0 += kTogether) {
-      float p[kTogether][N], q[INTER ? 1 : kTogether][N];
+    // all tokens' loads before the first store
+    float p[kTogether][N], q[INTER ? 1 : kTogether][N];
 #pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        const int ti = min(t0 + i, nt - 1);
-        get<BF>(x.p, fb[ti] + from, p[i]);
-        if constexpr (!INTER) get<BF>(x.p, fb[ti] + from + (copy ? 0 : half), q[i]);
-      }
+    for (int i = 0; i < kTogether; ++i) {
+      const int ti = min(t0 + i, nt - 1);
+      get<BF>(x.p, fb[ti] + from, p[i]);
+      if constexpr (!INTER) get<BF>(x.p, fb[ti] + from + (copy ? 0 : half), q[i]);
+    }
 #pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        const int ti = t0 + i;
-        if (ti >= nt) break;
-        if (!copy) {
-          if constexpr (INTER) {
+    for (int i = 0; i < kTogether; ++i) {
+      const int ti = t0 + i;
+      if (ti >= nt) break;
+      if (!copy) {
+        if constexpr (INTER) {
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-              const float2 e = cs[ti * half + N / 2 * u + j];
-              const float v = p[i][2 * j], z = p[i][2 * j + 1];
-              p[i][2 * j] = v * e.x - z * e.y;
-              p[i][2 * j + 1] = v * e.y + z * e.x;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-              const float2 e = cs[ti * half + N * u + j];
-              const float v = p[i][j];
-              p[i][j] = v * e.x - q[i][j] * e.y;
-              q[i][j] = v * e.y + q[i][j] * e.x;
-            }
-            put<BF>(out, tb[ti] + to + half, q[i]);
+          for (int j = 0; j < N / 2; ++j) {
+            const float2 e = cs[ti * half + N / 2 * u + j];
+            const float v = p[i][2 * j], z = p[i][2 * j + 1];
+            p[i][2 * j] = v * e.x - z * e.y;
+            p[i][2 * j + 1] = v * e.y + z * e.x;
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float2 e = cs[ti * half + N * u + j];
+            const float v = p[i][j];
+            p[i][j] = v * e.x - q[i][j] * e.y;
+            q[i][j] = v * e.y + q[i][j] * e.x;
+          }
+          put<BF>(out, tb[ti] + to + half, q[i]);
         }
-        put<BF>(out, tb[ti] + to, p[i]);
       }
+      put<BF>(out, tb[ti] + to, p[i]);
     }
   }
 }
@@ -160,18 +161,17 @@ auto kernel_for(const Rope& a) {
 hipError_t enqueue_rope(const Rope& a, hipStream_t s) {
   const int64_t n = a.B * a.T;
   const int64_t rows = a.k.p ? 2 * a.H : a.H;
-  // Sixteen tokens a workgroup, fewer where the angles would not fit or the
-  // card would not be filled; a token's rows are shared out if there are few.
+  // Tokens of a workgroup: about kRows rows (32768 tokens, 64 rows each, us, with
+  // 128 / 256 / 512 / 1024 rows: 97 / 97 / 103 / 111; 16 rows each 22.3 / 23.0 /
+  // 22.9 / 23.0), two at a time (2 / 4 / 8 at a time: 92 / 95 / 99), and
+  // one where the card would not be filled with 1024 workgroups (64 tokens: 3.6
+  // us, 8.1 with sixteen).  From 2^24 tokens on the grid would grow too large.
   int tokens = kMaxTokens;
-  while (tokens > 1 && (tokens * (a.R / 2) > kMaxAngles || n / tokens < 1024)) tokens /= 2;
-  int64_t shares = 1;
-  const int64_t groups = (n + tokens - 1) / tokens;
-  while (groups * shares < 512 && rows / (2 * shares) >= 8) shares *= 2;
-  const int share = (int)((rows + shares - 1) / shares);
-  const dim3 grid((unsigned)groups, (unsigned)((rows + share - 1) / share));
+  while (tokens > 1 && (n / tokens < 1024 || (tokens > kTogether && tokens * rows > kRows && n < (1 << 24)))) tokens /= 2;
+  const dim3 grid((unsigned)((n + tokens - 1) / tokens));
   auto* kernel = a.bf16 ? (a.interleaved ? kernel_for<true, true>(a) : kernel_for<true, false>(a))
                         : (a.interleaved ? kernel_for<false, true>(a) : kernel_for<false, false>(a));
-  hipLaunchKernelGGL(kernel, grid, dim3(NTR), 0, s, a, tokens, share);
+  hipLaunchKernelGGL(kernel, grid, dim3(NTR), 0, s, a, tokens);
   return hipGetLastError();
 }
 
