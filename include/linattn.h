@@ -169,7 +169,7 @@ int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const vo
  * is stored, so that linattn_rms_norm_bwd sees the same values.
  *
  *   rows, C   C is a multiple of 8 up to LINATTN_MAX_COLUMNS; at most 2^25
- *             rows, or 2^22 of more than 2048 columns
+ *             rows, or 2^21 of more than 1024 columns
  *   x, residual, h, y   [rows, C] of `dtype`, contiguous.  residual and h are
  *             both NULL (h = x) or both given; h may be x or residual itself.
  *   weight    C float32 values

@@ -272,9 +272,9 @@ int norm_sizes(int64_t rows, int64_t C, float eps, int dtype) {
   if (!(std::isfinite(eps) && eps >= 0.f)) return invalid("eps must be finite and >= 0");
   if (C % 8 || C > LINATTN_MAX_COLUMNS) return unsupported("C must be a multiple of 8 up to 16384");
   // a launch holds fewer than 2^32 work-items: 64 for each of many rows of up
-  // to 2048 columns, else up to 512
-  if (rows > (C <= 2048 ? 1 << 25 : 1 << 22))
-    return unsupported("rows exceed the supported number (2^25, or 2^22 of more than 2048 columns)");
+  // to 1024 columns, else up to 1024
+  if (rows > (C <= 1024 ? 1 << 25 : 1 << 21))
+    return unsupported("rows exceed the supported number (2^25, or 2^21 of more than 1024 columns)");
   return WKV6_OK;
 }
 

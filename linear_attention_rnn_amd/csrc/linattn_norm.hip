@@ -10,7 +10,7 @@
 // pieces of 8 adjacent columns each (16-byte loads of bfloat16), so a wave
 // reads 1 KiB at a time.  Sums are float32: a thread's own, then the wave's
 // by lane exchanges, then the waves' through LDS.  32768 rows of 2048 columns
-// in bfloat16 with a residual: 101 us, 5.3 TB/s; 256 rows with 8-bit codes 4 us,
+// in bfloat16 with a residual: 90 us, 6.0 TB/s; 256 rows with 8-bit codes 4 us,
 // a launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -350,19 +350,20 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, float*
   }
 }
 
-// Threads of a row and pieces of each, at most four (32 columns a thread): a
-// wave holds up to 512 columns, and up to 1024 of many rows, four waves up to
-// 8192, eight the rest.  Measured, us, a wave / four waves: 1024 columns of 256
-// rows 3.4 / 3.0, of 2048 rows 4.5 / 4.8, of 16384 rows 17.2 / 19.7; 2048
-// columns of 256 rows 4.5 / 3.1, of 16384 rows 32.7 / 31.2.
+// Threads of a row and pieces of each, at most two (16 columns a thread): a
+// wave holds up to 512 columns, and up to 1024 of many rows, then four, eight
+// and sixteen up to 4096, 8192 and 16384.  Measured, us, a wave / four waves:
+// 1024 columns of 256 rows 3.4 / 3.0, of 2048 rows 4.5 / 4.8, of 16384 rows 17.2
+// / 19.7; 2048 columns of 256 rows 4.5 / 3.1, of 16384 rows 32.7 / 31.2.  Four /
+// eight / sixteen: 4096 columns of 4096 float32 rows 32.0 / 32.8 / 32.0; 8192 of
+// 2048 rows 35.3 / 33.0 / 34.1; 16384 of 1024 rows, eight / sixteen 35.7 / 34.3.
 struct Shape {
   int tpr, nv;
 };
 Shape shape_of(int64_t rows, int64_t C) {
   const int64_t pieces = C / 8;
-  const int tpr = pieces <= 64 || (pieces <= 128 && rows >= 2048) ? 64 : pieces <= 1024 ? 256 : 512;
-  const int64_t need = (pieces + tpr - 1) / tpr;
-  return {tpr, need <= 1 ? 1 : need <= 2 ? 2 : 4};
+  const int tpr = pieces <= 64 || (pieces <= 128 && rows >= 2048) ? 64 : pieces <= 512 ? 256 : pieces <= 1024 ? 512 : 1024;
+  return {tpr, pieces <= tpr ? 1 : 2};
 }
 
 // The gradients keep the next row and the sums of dweight besides: at most two
@@ -405,8 +406,9 @@ int bwd_groups(const NormBwd& a, const Shape& f) {
 hipError_t enqueue_norm(const Norm& a, hipStream_t s) {
   const Shape f = shape_of(a.rows, a.C);
   const auto launch = f.tpr == 64    ? (f.nv == 1 ? launch_norm<64, 1> : launch_norm<64, 2>)
-                      : f.tpr == 256 ? (f.nv == 1 ? launch_norm<256, 1> : f.nv == 2 ? launch_norm<256, 2> : launch_norm<256, 4>)
-                                     : launch_norm<512, 4>;
+                      : f.tpr == 256 ? (f.nv == 1 ? launch_norm<256, 1> : launch_norm<256, 2>)
+                      : f.tpr == 512 ? launch_norm<512, 2>
+                                     : launch_norm<1024, 2>;
   launch(a, s);
   return hipGetLastError();
 }

@@ -172,7 +172,7 @@ def norm_bwd(rows=4, C=256, eps=1e-5, dtype=1, ws=(0, 0), **p):
 
 
 SIZES = [(dict(rows=-1), INVALID), (dict(C=0), INVALID), (dict(C=100), UNSUPPORTED), (dict(C=16392), UNSUPPORTED),
-         (dict(rows=2 ** 25 + 1), UNSUPPORTED), (dict(rows=2 ** 22 + 1, C=2056), UNSUPPORTED), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+         (dict(rows=2 ** 25 + 1), UNSUPPORTED), (dict(rows=2 ** 21 + 1, C=1032), UNSUPPORTED), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
          (dict(eps=float("inf")), INVALID), (dict(dtype=4), INVALID)]
 
 
