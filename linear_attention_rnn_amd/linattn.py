@@ -81,8 +81,8 @@ def bwd_workspace_bytes(B, T, H, K, V, dtype=torch.bfloat16, grad_dtype=torch.fl
 
 # ---------------------------------------------------------------- checks
 # These run before every call and are most of what a call costs the host next
-# to the launch itself (3.5 us of 7 for a single-token step), hence few and
-# plain expressions.
+# to the launch itself (3 us of 6.5 for a single-token step), hence few and
+# plain expressions, and none for tensors made here.
 def _dtype(t, name):
     d = _DTYPES.get(t.dtype)
     if d is None:
@@ -126,6 +126,7 @@ def _strides(*tensors):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name, f, device, stream, *args):
@@ -135,7 +136,7 @@ def _call(name, f, device, stream, *args):
         handle = _raw_stream(device.index)
     else:
         handle = _stream_handle(stream, device)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         status = f(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -200,14 +201,20 @@ def fwd(q, k, v, log_decay, scale: float = 1.0, lengths=None, s_in=None, want_st
     B, T, H, K, V, dtype, dev, pq, pk, pv, pg, pl = _attention(q, k, v, log_decay, lengths)
     if out is None:
         out = torch.empty((B, T, H, V), dtype=out_dtype or q.dtype, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out must have out_dtype")
+        py = out.data_ptr()
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must have out_dtype")
+        py = _tensor(out, "out", (B, T, H, V), out.dtype, dev)
     odt = _dtype(out, "out")
-    py = _tensor(out, "out", (B, T, H, V), out.dtype, dev)
     ps = _flat(s_in, "s_in", (B, H, K, V), torch.float32, dev)
-    if s_out is None and want_state:
+    if s_out is not None:
+        po = ps if s_out is s_in else _flat(s_out, "s_out", (B, H, K, V), torch.float32, dev)
+    elif want_state:
         s_out = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
-    po = _flat(s_out, "s_out", (B, H, K, V), torch.float32, dev)
+        po = s_out.data_ptr()
+    else:
+        po = 0
     L = lib()
     pw, nw, keep = _NO_WORKSPACE if T <= _STEP_TOKENS else _workspace(
         workspace, lambda: L.linattn_fwd_workspace_bytes(B, T, H, K, V, dtype, odt, po != 0), dev, stream)
@@ -310,13 +317,17 @@ def rope(q, k, freqs, positions=None, start: int = 0, layout: str = "half", inve
     pp = _flat(positions, "positions", (B, T), torch.int32, dev)
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    pqo = _tensor(q_out, "q_out", shape, t, dev)
+        pqo = q_out.data_ptr()
+    else:
+        pqo = pq if q_out is q else _tensor(q_out, "q_out", shape, t, dev)
     pk = pko = 0
     if k is not None:
         pk = _tensor(k, "k", shape, t, dev)
         if k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        pko = _tensor(k_out, "k_out", shape, t, dev)
+            pko = k_out.data_ptr()
+        else:
+            pko = pk if k_out is k else _tensor(k_out, "k_out", shape, t, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
     _call("linattn_rope", lib().linattn_rope, dev, stream, B, T, H, D, 2 * freqs.shape[0], pq, pk, pqo, pko, pp, start,
@@ -372,6 +383,7 @@ def _residual(x, residual, h):
     pr = _flat(residual, "residual", x.shape, x.dtype, x.device)
     if h is None:
         h = torch.empty_like(x)
+        return h, pr, h.data_ptr()
     return h, pr, _flat(h, "h", x.shape, x.dtype, x.device)
 
 
@@ -385,7 +397,9 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, h=None, out=None, stre
     h, pr, ph = _residual(x, residual, h)
     if out is None:
         out = torch.empty_like(x)
-    py = _flat(out, "out", x.shape, x.dtype, dev)
+        py = out.data_ptr()
+    else:
+        py = _flat(out, "out", x.shape, x.dtype, dev)
     _call("linattn_rms_norm", lib().linattn_rms_norm, dev, stream, rows, C, x.data_ptr(), pr, pw, eps, ph, py, dtype)
     return out, h
 
@@ -401,11 +415,15 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, group: int = 128, h
     h, pr, ph = _residual(x, residual, h)
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    pc = _flat(codes, "codes", x.shape, torch.float8_e4m3fn, dev)
+        pc = codes.data_ptr()
+    else:
+        pc = _flat(codes, "codes", x.shape, torch.float8_e4m3fn, dev)
     shape = (*x.shape[:-1], (C + 127) // 128 if group else 1)
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=dev)
-    ps = _flat(scales, "scales", shape, torch.float32, dev)
+        ps = scales.data_ptr()
+    else:
+        ps = _flat(scales, "scales", shape, torch.float32, dev)
     _call("linattn_rms_norm_q8", lib().linattn_rms_norm_q8, dev, stream, rows, C, x.data_ptr(), pr, pw, eps, ph, pc, ps,
           group, dtype)
     return codes, scales, h
@@ -422,7 +440,9 @@ def rms_norm_bwd(dy, h, weight, eps: float = 1e-6, dh=None, out=None, workspace=
         raise ValueError("dy is missing")
     if out is None:
         out = torch.empty_like(h)
-    px = _flat(out, "out", h.shape, h.dtype, dev)
+        px = out.data_ptr()
+    else:
+        px = _flat(out, "out", h.shape, h.dtype, dev)
     dweight = torch.empty((C,), dtype=torch.float32, device=dev)
     L = lib()
     pws, nws, keep = _workspace(workspace, lambda: L.linattn_rms_norm_bwd_workspace_bytes(rows, C, dtype), dev, stream)
