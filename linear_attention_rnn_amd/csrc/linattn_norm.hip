@@ -110,7 +110,7 @@ __device__ __forceinline__ float over_lanes(float x) {
 // ... over the TPR threads of a row; `lds`: 16 floats that no one else uses.
 template <int TPR, bool MAX>
 __device__ __forceinline__ float over_row(float x, float* lds) {
-  x = over_lanes<64, MAX>(x);
+  x = over_lanes<(TPR < 64 ? TPR : 64), MAX>(x);
   if constexpr (TPR > 64) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(Norm a) {
   __shared__ float lds[2][16];
   const int at = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
-  if (row >= a.rows) return;   // whole waves: TPR is a multiple of 64
+  if (row >= a.rows) return;   // all threads of a row together
   const int64_t base = row * a.C;
   float h[NV][8];
   float sum = 0.f;
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(Norm a) {
       for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[v][j]));
       if constexpr (OUT == 1) {
         // 16 lanes hold 128 adjacent columns
-        top = over_lanes<16, true>(top);
+        top = over_lanes<(TPR < 16 ? TPR : 16), true>(top);
         const float scale = scale_of(top);
         if (c < a.C) {
           if ((at & 15) == 0) a.scales[row * ((a.C + 127) / 128) + c / 128] = scale;
@@ -237,7 +237,7 @@ template <int TPR, int NV, bool BF>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd a, float* part) {
   constexpr int NT = TPR > 256 ? TPR : 256, RW = NT / TPR;
   __shared__ float lds[2][2][16];
-  __shared__ float join[RW > 1 ? TPR * NV * 8 : 1];
+  __shared__ float join[RW > 1 ? RW : 1][RW > 1 ? TPR * NV * 8 : 1];
   const int at = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   float dw[NV][8], wt[NV][8];
 #pragma unroll
@@ -306,29 +306,22 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     }
   }
   if constexpr (RW > 1) {
-    for (int s = 0; s < RW; ++s) {
-      if (slot == s)
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) put8<false>(join[slot], (v * TPR + at) * 8, dw[v]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.C; c += NT) {
+      float q = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float& q = join[(v * 8 + j) * TPR + at];
-            q = s == 0 ? dw[v][j] : q + dw[v][j];
-          }
-      __syncthreads();
+      for (int s = 0; s < RW; ++s) q += join[s][c];
+      part[blockIdx.x * a.C + c] = q;
     }
-    if (slot == 0)
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[v][j] = join[(v * 8 + j) * TPR + at];
-  }
-  if (slot == 0)
+  } else {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;
       if (c < a.C) put8<false>(part, blockIdx.x * a.C + c, dw[v]);
     }
+  }
 }
 
 // dweight of 16 columns: the workgroups' sums in 64 interleaved shares, the
@@ -354,9 +347,11 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, float*
   }
 }
 
-// Threads of a row and pieces of each, at most two (16 columns a thread): a
-// wave holds up to 512 columns, and up to 1024 of many rows, then four, eight
-// and sixteen up to 4096, 8192 and 16384.  Measured, us, a wave / four waves:
+// Threads of a row and pieces of each, at most two (16 columns a thread): 8, 16
+// and 32 threads hold up to 64, 128 and 256 columns, a wave up to 512, and up to
+// 1024 of many rows, then four, eight and sixteen waves up to 4096, 8192 and
+// 16384.  Measured, us, a wave / fewer threads: 64 columns of 2^19 rows 96 / 22,
+// 128 of 2^18 50 / 22, 256 of 2^17 30 / 22.  Then, us, a wave / four waves:
 // 1024 columns of 256 rows 3.4 / 3.0, of 2048 rows 4.5 / 4.8, of 16384 rows 17.2
 // / 19.7; 2048 columns of 256 rows 4.5 / 3.1, of 16384 rows 32.7 / 31.2.  Four /
 // eight / sixteen: 4096 columns of 4096 float32 rows 32.0 / 32.8 / 32.0; 8192 of
@@ -366,16 +361,17 @@ struct Shape {
 };
 Shape shape_of(int64_t rows, int64_t C) {
   const int64_t pieces = C / 8;
-  const int tpr = pieces <= 64 || (pieces <= 128 && rows >= 2048) ? 64 : pieces <= 512 ? 256 : pieces <= 1024 ? 512 : 1024;
+  const int tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 64 || (pieces <= 128 && rows >= 2048) ? 64 : pieces <= 512 ? 256 : pieces <= 1024 ? 512 : 1024;
   return {tpr, pieces <= tpr ? 1 : 2};
 }
 
 // The gradients keep the next row and the sums of dweight besides: at most two
-// pieces a thread up to 8192 columns.  A wave / four waves, us: 1024 columns of
+// pieces a thread up to 8192 columns.  A wave / fewer threads, us: 64 columns of
+// 2^19 rows 223 / 35, 256 of 2^17 62 / 37; a wave / four waves: 1024 columns of
 // 256 rows 6.1 / 7.0, of 16384 rows 19.4 / 37.7.
 Shape bwd_shape_of(int64_t C) {
   const int64_t pieces = C / 8;
-  const int tpr = pieces <= 128 ? 64 : pieces <= 512 ? 256 : 512;
+  const int tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 128 ? 64 : pieces <= 512 ? 256 : 512;
   const int64_t need = (pieces + tpr - 1) / tpr;
   return {tpr, need <= 1 ? 1 : need <= 2 ? 2 : 4};
 }
@@ -403,7 +399,7 @@ void launch_norm_bwd(const NormBwd& a, float* part, int groups, hipStream_t s) {
 // 28.5; 4096 float32 rows of 8192 95.8 / 102 / 122.  Two rows for each at
 // least costs small calls more than it saves (64 x 1024 6.1 -> 6.9 us).
 int bwd_groups(const NormBwd& a, const Shape& f) {
-  const int rw = f.tpr >= 256 ? 1 : 4, most = f.tpr >= 512 ? 256 : 512;
+  const int rw = f.tpr >= 256 ? 1 : 256 / f.tpr, most = f.tpr >= 512 ? 256 : 512;
   const int64_t want = (a.rows + rw - 1) / rw;
   return (int)(want < most ? want : most);
 }
@@ -412,7 +408,10 @@ int bwd_groups(const NormBwd& a, const Shape& f) {
 
 hipError_t enqueue_norm(const Norm& a, hipStream_t s) {
   const Shape f = shape_of(a.rows, a.C);
-  const auto launch = f.tpr == 64    ? (f.nv == 1 ? launch_norm<64, 1> : launch_norm<64, 2>)
+  const auto launch = f.tpr == 8     ? launch_norm<8, 1>
+                      : f.tpr == 16  ? launch_norm<16, 1>
+                      : f.tpr == 32  ? launch_norm<32, 1>
+                      : f.tpr == 64  ? (f.nv == 1 ? launch_norm<64, 1> : launch_norm<64, 2>)
                       : f.tpr == 256 ? (f.nv == 1 ? launch_norm<256, 1> : launch_norm<256, 2>)
                       : f.tpr == 512 ? launch_norm<512, 2>
                                      : launch_norm<1024, 2>;
@@ -426,7 +425,10 @@ hipError_t enqueue_norm_bwd(const NormBwd& a, void* workspace, hipStream_t s) {
   const Shape f = bwd_shape_of(a.C);
   const int groups = bwd_groups(a, f);
   float* part = static_cast<float*>(workspace);
-  const auto launch = f.tpr == 64    ? (f.nv == 1 ? launch_norm_bwd<64, 1> : launch_norm_bwd<64, 2>)
+  const auto launch = f.tpr == 8     ? launch_norm_bwd<8, 1>
+                      : f.tpr == 16  ? launch_norm_bwd<16, 1>
+                      : f.tpr == 32  ? launch_norm_bwd<32, 1>
+                      : f.tpr == 64  ? (f.nv == 1 ? launch_norm_bwd<64, 1> : launch_norm_bwd<64, 2>)
                       : f.tpr == 256 ? (f.nv == 1 ? launch_norm_bwd<256, 1> : launch_norm_bwd<256, 2>)
                                      : (f.nv <= 2 ? launch_norm_bwd<512, 2> : launch_norm_bwd<512, 4>);
   if (groups) launch(a, part, groups, s);

@@ -17,7 +17,7 @@ from tests.linattn_util import BF, TYPES, U, bits, f64, generator, normal, say
 
 pytestmark = pytest.mark.gpu
 
-SHAPES = [(1, 8), (3, 64), (5, 504), (7, 520), (300, 2048), (2500, 2048), (2500, 1032), (4, 4104), (9, 8192), (2, 8200),
+SHAPES = [(1, 8), (3, 64), (33, 72), (100, 128), (19, 136), (65, 256), (35, 264), (5, 504), (7, 520), (300, 2048), (2500, 2048), (2500, 1032), (4, 4104), (9, 8192), (2, 8200),
           (3, 16384), (2100, 512)]
 
 
