@@ -48,6 +48,8 @@ struct Sweep {
   bool out_bf16;
 };
 
+__host__ __device__ inline int vblocks_of(const Sweep& a) { return (a.V + kVBlock - 1) / kVBlock; }
+
 // Up to three sweeps over the same sequences, types and product K V, run side
 // by side: none reads what another writes, except that the last one's s_out
 // may be another one's s_in.
@@ -65,6 +67,7 @@ struct SweepPlan {
   int segments;     // of each sequence
   int seg_tokens;   // tokens of a segment, a multiple of 64
   int vblocks;      // blocks of 64 value channels, the most of the sweeps
+  int blocks;       // blocks of value channels of all sweeps
   int64_t pairs;    // B H
   int64_t items;    // pairs * segments
 };

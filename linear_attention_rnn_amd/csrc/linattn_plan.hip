@@ -101,7 +101,7 @@ __global__ __launch_bounds__(NTH) void state_copy_kernel(const float4* from, flo
 
 template <int KX>
 hipError_t launch_steps(const Sweep& a, hipStream_t s) {
-  const int vblocks = (a.V + kVBlock - 1) / kVBlock;
+  const int vblocks = vblocks_of(a);
   const dim3 grid((unsigned)(a.B * a.H * vblocks));
   if (!a.bf16)
     hipLaunchKernelGGL((step_kernel<KX, false, false>), grid, dim3(NTH), 0, s, a, vblocks);
@@ -129,7 +129,7 @@ SweepPlan plan(const Sweep* a, int n) {
   for (int i = 0; i < n; ++i) {
     p.a[i] = a[i];
     p.state_out = p.state_out || a[i].s_out;
-    const int vb = (a[i].V + kVBlock - 1) / kVBlock;
+    const int vb = vblocks_of(a[i]);
     p.vblocks = std::max(p.vblocks, vb);
     blocks += vb;
   }

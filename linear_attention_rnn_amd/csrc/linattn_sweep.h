@@ -217,13 +217,17 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
   __shared__ __bf16 Sp[SUMMARY ? 8 : MP * KP * 64];
 
   // The sweeps and blocks of values of one item, which read the same rows, are
-  // 8 apart, so that they run on one XCD and share its L2.
-  const int kinds = p.vblocks * p.sweeps;
-  const int64_t item = (int64_t)(blockIdx.x / (8 * kinds)) * 8 + blockIdx.x % 8;
-  const int kind = blockIdx.x / 8 % kinds, sweep = kind / p.vblocks, vb = kind % p.vblocks, v0 = vb * kVBlock;
+  // 8 apart, so that they run on one XCD and share its L2.  None is without
+  // work: workgroups go to the shader engines in turn whatever they do, and
+  // idle ones in a pattern left some engines two rounds and others none
+  // (float32 gradients of K = 64, V = 96: 144 us, now 82).
+  const int64_t item = (int64_t)(blockIdx.x / (8 * p.blocks)) * 8 + blockIdx.x % 8;
+  int sweep = 0, vb = blockIdx.x / 8 % p.blocks;
+  for (int i = 0; i + 1 < kSweeps && vb >= vblocks_of(p.a[sweep]); ++i) vb -= vblocks_of(p.a[sweep++]);
+  const int v0 = vb * kVBlock;
   const Sweep& a = p.a[sweep];
   const bool rev = a.reverse;
-  if (item >= p.items || v0 >= a.V) return;
+  if (item >= p.items) return;
   const int segs = SUMMARY ? p.segments - 1 : p.segments;
   const int64_t pair = item / segs;
   const int seg = (int)(item % segs);
@@ -547,8 +551,11 @@ __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
 }
 
 template <int KP, bool BF, int MP, int UP, bool OBF>
-hipError_t launch(const SweepPlan& p, hipStream_t s) {
-  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.vblocks * p.sweeps)); };
+hipError_t launch(const SweepPlan& of, hipStream_t s) {
+  SweepPlan p = of;
+  p.blocks = 0;
+  for (int i = 0; i < p.sweeps; ++i) p.blocks += vblocks_of(p.a[i]);
+  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.blocks)); };
   if (p.segments > 1) {
     SweepPlan q = p;
     q.items = p.pairs * (p.segments - 1);
