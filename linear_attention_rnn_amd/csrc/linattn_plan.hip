@@ -137,17 +137,20 @@ SweepPlan plan(const Sweep* a, int n) {
   const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * blocks;
   // Segments cost a second pass over keys and values, so they are for calls
   // that leave CUs idle: below 160 workgroups, up to two for each of the 256
-  // CUs, of at least four chunks (float32, whose chunks take three times as
-  // long: two).  Measured, us, with 1 / 4 / 8 / 16 / 64 segments: 192
-  // workgroups (gradients, 64 chunks) 101 / 108 / 119 / 129 / 240; 64 of them
-  // (64 chunks) 155 / 77 / 73 / 78 / 116; 32 (128 chunks of K = V = 128)
-  // 301 / 139 / 88 / 81 / 121; 2 (256 chunks) 380 / 171 / 95 / 58 / 36, and
-  // 41 with 128.  A CU holds one workgroup of the float32 sweeps of more than
-  // 64 key channels at a time, so those stay in one round of 256 (gradients
-  // of K = 128, V = 64, 13 chunks: 73 us with 3 segments, 80 with 5).
+  // CUs.  Measured, us, with 1 / 4 / 8 / 16 / 64 segments: 192 workgroups
+  // (gradients, 64 chunks) 101 / 108 / 119 / 129 / 240; 64 of them (64 chunks)
+  // 155 / 77 / 73 / 78 / 116; 32 (128 chunks of K = V = 128) 301 / 139 / 88 / 81 /
+  // 121; 2 (256 chunks) 380 / 171 / 95 / 58 / 36, and 41 with 128.  They have
+  // three chunks at least, for calls of eight (8 heads, us, two / three / four
+  // chunks: of 512 tokens 15.3 / 15.9 / 19.4, of 1024 17.1 / 16.5 / 19.9, of 4096
+  // 24.3 / 22.5 / 24.3; 5 chunks, one segment / two: 15.0 / 18.6); two where
+  // chunks take longer, in float32.  A CU holds one workgroup of the float32
+  // sweeps of more than 64 key channels at a time, so those stay in one round
+  // of 256 (gradients of K = 128, V = 64, 13 chunks: 73 us with 3 segments, 80
+  // with 5).
   int64_t G = groups >= 160 ? 1 : (512 + groups - 1) / groups;
   if (!a->bf16 && widest(a, n) > 64 && G > 1) G = 256 / groups;
-  G = std::max<int64_t>(1, std::min(G, chunks / (a->bf16 ? 4 : 2)));
+  G = std::max<int64_t>(1, std::min(G, !a->bf16 ? chunks / 2 : chunks < 8 ? 1 : (chunks + 2) / 3));
   const int64_t per = (chunks + G - 1) / G;
   p.seg_tokens = (int)(per * kChunk);
   p.segments = (int)((chunks + per - 1) / per);
