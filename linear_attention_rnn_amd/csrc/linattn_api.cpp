@@ -288,7 +288,8 @@ size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
                                    int state_out) try {
   set_error(WKV6_OK, "");
   if (check_sizes(B, T, H, K, V, dtype, out_dtype) != WKV6_OK || B == 0 || T == 0) return 0;
-  linattn::Sweep a = base_sweep(B, T, H, K, V, nullptr, nullptr, dtype, out_dtype);
+  const int32_t some = 0;   // (calls with lengths take as much as others or more)
+  linattn::Sweep a = base_sweep(B, T, H, K, V, nullptr, &some, dtype, out_dtype);
   float any = 0.f;
   a.s_out = state_out ? &any : nullptr;
   return linattn::sweep_workspace_bytes(&a, 1);
@@ -343,7 +344,8 @@ size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
   const Tensor none[7] = {};
   linattn::Sweep w[3];
   float any = 0.f;
-  bwd_sweeps(B, T, H, K, V, nullptr, 1.f, nullptr, nullptr, nullptr, state_grad ? &any : nullptr, none, dtype, grad_dtype, w);
+  const int32_t some = 0;
+  bwd_sweeps(B, T, H, K, V, nullptr, 1.f, &some, nullptr, nullptr, state_grad ? &any : nullptr, none, dtype, grad_dtype, w);
   return linattn::sweep_workspace_bytes(w, 3);
 } catch (...) {
   return 0;

@@ -137,7 +137,10 @@ SweepPlan plan(const Sweep* a, int n) {
   const int64_t chunks = (a->T + kChunk - 1) / kChunk, groups = p.pairs * blocks;
   // Segments cost a second pass over keys and values, so they are for calls
   // that leave CUs idle: below 160 workgroups, up to two for each of the 256
-  // CUs.  Measured, us, with 1 / 4 / 8 / 16 / 64 segments: 192 workgroups
+  // CUs, and with lengths, which leave later segments short or empty, up to the
+  // next multiple (float32 gradients of 24 heads, 72 workgroups: 7 segments 82,
+  // 8 101; 7 x 4880 tokens of 16 heads with lengths: 4 segments 201, 5 174).
+  // Otherwise measured, us, with 1 / 4 / 8 / 16 / 64 segments: 192 workgroups
   // (gradients, 64 chunks) 101 / 108 / 119 / 129 / 240; 64 of them (64 chunks)
   // 155 / 77 / 73 / 78 / 116; 32 (128 chunks of K = V = 128) 301 / 139 / 88 / 81 /
   // 121; 2 (256 chunks) 380 / 171 / 95 / 58 / 36, and 41 with 128.  They have
@@ -148,7 +151,7 @@ SweepPlan plan(const Sweep* a, int n) {
   // sweeps of more than 64 key channels at a time, so those stay in one round
   // of 256 (gradients of K = 128, V = 64, 13 chunks: 73 us with 3 segments, 80
   // with 5).
-  int64_t G = groups >= 160 ? 1 : (512 + groups - 1) / groups;
+  int64_t G = groups >= 160 ? 1 : (512 + (a->lengths ? groups - 1 : 0)) / groups;
   if (!a->bf16 && widest(a, n) > 64 && G > 1) G = 256 / groups;
   G = std::max<int64_t>(1, std::min(G, !a->bf16 ? chunks / 2 : chunks < 8 ? 1 : (chunks + 2) / 3));
   const int64_t per = (chunks + G - 1) / G;
