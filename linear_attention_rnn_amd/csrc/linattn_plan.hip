@@ -121,6 +121,34 @@ int widest(const Sweep* a, int n) {
   return K;
 }
 
+// Sweeps of at most and of more than 64 key channels in launches of their own,
+// the last sweep's second: float32 gradients of more than one round of
+// workgroups, for the narrow ones take two thirds of the time and two fit a CU.
+// Us, together / so, of 4 x 1000 tokens, 32 heads of 128 x 64 (640 workgroups)
+// 321 / 210, 15 x 2064, 8 of 32 x 96 (480) 440 / 369, 14 x 40, 12 of 128 x 32 36.9
+// / 28.0; with fewer than 256 (2 x 777, 8 of 128 x 64) 58 / 73; in bfloat16, 8 x
+// 512 tokens, 16 of 64 x 128 53 / 62, 15 x 2064, 8 of 32 x 96 171 / 200.
+struct Split {
+  Sweep a[2][kSweeps];
+  int n[2] = {0, 0};
+};
+Split split(const Sweep* a, int n) {
+  Split s;
+  int64_t groups = 0;
+  bool wide = false, narrow = false;
+  for (int i = 0; i < n; ++i) {
+    groups += vblocks_of(a[i]) * a->B * a->H;
+    (a[i].K > 64 ? wide : narrow) = true;
+  }
+  if (a->bf16 || !wide || !narrow || groups <= 256) return s;
+  const bool last = a[n - 1].K > 64;
+  for (int i = 0; i < n; ++i) {
+    const int g = (a[i].K > 64) == last;
+    s.a[g][s.n[g]++] = a[i];
+  }
+  return s;
+}
+
 SweepPlan plan(const Sweep* a, int n) {
   SweepPlan p = {};
   p.sweeps = n;
@@ -173,6 +201,8 @@ hipError_t enqueue_state_copy(const float* from, float* to, int64_t n, hipStream
 
 size_t sweep_workspace_bytes(const Sweep* a, int n) {
   if (steps(a, n)) return 0;
+  if (const Split s = split(a, n); s.n[0])
+    return std::max(sweep_workspace_bytes(s.a[0], s.n[0]), sweep_workspace_bytes(s.a[1], s.n[1]));
   const SweepPlan p = plan(a, n);
   if (p.segments == 1) return 0;
   return (size_t)n * p.items * (widest(a, n) <= 64 ? 64 : 128) * kVBlock * p.vblocks * 4;
@@ -180,6 +210,10 @@ size_t sweep_workspace_bytes(const Sweep* a, int n) {
 
 hipError_t enqueue_sweeps(const Sweep* a, int n, void* workspace, hipStream_t s) {
   if (steps(a, n)) return a->K <= 64 ? launch_steps<4>(*a, s) : launch_steps<8>(*a, s);
+  if (const Split of = split(a, n); of.n[0]) {
+    const hipError_t e = enqueue_sweeps(of.a[0], of.n[0], workspace, s);
+    return e == hipSuccess ? enqueue_sweeps(of.a[1], of.n[1], workspace, s) : e;
+  }
   SweepPlan p = plan(a, n);
   if (p.segments > 1) p.ws = static_cast<float*>(workspace);
   const auto launch = widest(a, n) <= 64 ? launch_sweeps64 : launch_sweeps128;

@@ -186,6 +186,9 @@ __device__ __forceinline__ float tokens_in(const SweepPlan& p, int64_t len, int 
 // 79.8 / 73.7, 128 40.3 / 31.0.
 constexpr int kJoin = 8;
 
+// Waves a SIMD that the registers leave room for: three of the bfloat16 sweeps
+// of 64 key channels (166 registers; a fourth would spill), else two, which LDS
+// allows as well (float32: 74 KB a workgroup of 64 key channels, 123 KB of 128).
 template <int KP, bool BF, int MP>
 constexpr int occupancy() {
   return KP == 64 ? (BF && MP == 1 ? 3 : 2) : 2;

@@ -127,6 +127,22 @@ def test_layouts_do_not_matter(linattn, T):  # noqa: F811
         assert bits(a[n], b[n]), n
 
 
+@pytest.mark.parametrize("K,V", [(128, 40), (40, 128)])
+def test_wide_and_narrow_sweeps(linattn, K, V):  # noqa: F811
+    """Many float32 heads whose keys and values differ in width; states in place."""
+    B, T, H = 20, 300, 5
+    x = with_gradients(inputs(7, B, T, H, K, V, "f32"), 8, "f32")
+    d = cuda(x)
+    ds = d["ds_out"].clone()
+    g = call(linattn, dict(d, ds_out=ds), 0.7, out={"s_in": ds}, grad_dtype=torch.float32)
+    want = call(linattn, d, 0.7, want_ds_in=True, grad_dtype=torch.float32)
+    torch.cuda.synchronize()
+    ref, size = reference(x, 0.7)
+    for n in ref:
+        assert bits(g[n], want[n]), n
+        check(f"d{n}", g[n], ref[n], size[n], T, 128, False)
+
+
 def test_no_tokens(linattn):  # noqa: F811
     x = cuda(with_gradients(inputs(1, 2, 1, 2, 64, 32, "bf16"), 1, "bf16"))
     e = dict(x, **{n: x[n][:, :0] for n in ("q", "k", "v", "do")})
