@@ -14,11 +14,11 @@
 // A workgroup of four waves (eight: see waves()) runs one (batch item, head,
 // block of 64 value channels, segment).  Wave w computes the outputs of tokens
 // 16w..16w+15 (all 64 channels, transposed: O^T[n][t]) and keeps the state's
-// columns of its strip of 16 value channels in registers.  MFMA operands chain without a
-// detour: scores come out as K Q^T tiles whose accumulator lanes are, tile
-// pairs taken together, the operand lanes of the product with V^T; the state's
-// accumulators are the operand lanes of the product with q.  Only the state
-// crosses waves, through LDS as ready-made operand fragments.
+// columns of its strip of 16 value channels in registers.  MFMA operands chain
+// without a detour: scores come out as K Q^T tiles whose accumulator lanes are,
+// tile pairs taken together, the operand lanes of the product with V^T; the
+// state's accumulators are the operand lanes of the product with q.  Only the
+// state crosses waves, through LDS as ready-made operand fragments.
 //
 // The rows of an MFMA tile may be any 16 channels as long as both sides of a
 // product agree: "tile pairs" (2u, 2u+1) hold channels 32u + 8(m/4) + m%4 and
@@ -40,12 +40,12 @@
 // GB (the sweeps run both ways, so q, k, v and d_o come from memory nearly
 // twice), 4.4 TB/s.  With fewer workgroups than CUs a chunk's own chain of
 // steps sets the time, 3300 cycles of K = V = 64 and 5300 of K = 128 (float32:
-// three to four times that, for six products of parts).  Measured without gain: blocks of 32 value
-// channels, chunks of 128 tokens with eight waves (gradients of 64 heads: 103
-// -> 113 us), eight waves of bfloat16 heads (103 -> 110), waves with roles of
-// their own for outputs and state (126 -> 148), LDS places without any bank
-// conflict (no change), loads two chunks ahead, streaming loads and stores
-// (126 -> 139).
+// three to four times that, for six products of parts).  Measured without gain:
+// blocks of 32 value channels, chunks of 128 tokens with eight waves (gradients
+// of 64 heads: 103 -> 113 us), eight waves of bfloat16 heads (103 -> 110),
+// waves with roles of their own for outputs and state (126 -> 148), LDS places
+// without any bank conflict (no change), loads two chunks ahead, streaming
+// loads and stores (126 -> 139).
 #pragma once
 
 #include "linattn_internal.h"
