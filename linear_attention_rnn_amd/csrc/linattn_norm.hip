@@ -325,7 +325,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
 }
 
 // dweight of 16 columns: the workgroups' sums in 64 interleaved shares, the
-// shares in order.
+// shares by eights (in one chain their roundings would add up to twice as much).
 __global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, float* dweight, int groups, int64_t C) {
   __shared__ float lds[64][16];
   const int q = threadIdx.x % 4, s = threadIdx.x / 4;
@@ -342,7 +342,12 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, float*
   if (threadIdx.x < 16 && (int64_t)blockIdx.x * 16 + threadIdx.x < C) {
     float y = 0.f;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) y += lds[i][threadIdx.x];
+    for (int i = 0; i < 64; i += 8) {
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z += lds[i + j][threadIdx.x];
+      y += z;
+    }
     dweight[(int64_t)blockIdx.x * 16 + threadIdx.x] = y;
   }
 }
