@@ -13,6 +13,11 @@ namespace {
 // rows y, y + 16, .. of columns 4x..4x+3.  Bound by the state's bytes, read
 // and written once as whole 256-byte rows: one token of 256 x 32 heads of 64 x
 // 64, 50 us, 5.4 TB/s; of 12 heads 4 us, a launch.
+//
+// The decay is carried in two parts, a = hi + lo: rounded to float32 it would
+// be off the same way at every token, and a state that lives for 1 / (1 - a)
+// tokens by as many times 2^-25 (6e-5 after 4096 tokens with a = 1 - 10^-5).
+// Both parts are positive, so that an infinite state stays what it is.
 template <int KX, bool BF, bool OBF>
 __global__ __launch_bounds__(NTH) void step_kernel(Sweep a, int vblocks) {
   __shared__ float qk[2][kStepTokens][16 * KX];
@@ -24,7 +29,10 @@ __global__ __launch_bounds__(NTH) void step_kernel(Sweep a, int vblocks) {
   const int n = v0 + 4 * x;
   const bool live = n < a.V;
   const int T = (int)tokens_of(a, b);
-  const float decay = ex2(log2_decay(a.log_decay[h]));
+  const double decay = exp((double)a.log_decay[h]);
+  float hi = (float)decay;
+  if ((double)hi >= decay && hi > 0.f) hi = __uint_as_float(__float_as_uint(hi) - 1);   // the next float32 below
+  const float lo = (float)(decay - (double)hi);
 
   const auto value = [](const void* p, int64_t i) {
     if constexpr (BF)
@@ -54,10 +62,10 @@ __global__ __launch_bounds__(NTH) void step_kernel(Sweep a, int vblocks) {
 #pragma unroll
     for (int i = 0; i < KX; ++i) {
       const float k = qk[1][t][y + 16 * i], q = qk[0][t][y + 16 * i];
-      M[i].x = fmaf(decay, M[i].x, k * v.x);
-      M[i].y = fmaf(decay, M[i].y, k * v.y);
-      M[i].z = fmaf(decay, M[i].z, k * v.z);
-      M[i].w = fmaf(decay, M[i].w, k * v.w);
+      M[i].x = fmaf(hi, M[i].x, fmaf(lo, M[i].x, k * v.x));
+      M[i].y = fmaf(hi, M[i].y, fmaf(lo, M[i].y, k * v.y));
+      M[i].z = fmaf(hi, M[i].z, fmaf(lo, M[i].z, k * v.z));
+      M[i].w = fmaf(hi, M[i].w, fmaf(lo, M[i].w, k * v.w));
       o.x = fmaf(q, M[i].x, o.x);
       o.y = fmaf(q, M[i].y, o.y);
       o.z = fmaf(q, M[i].z, o.z);

@@ -77,6 +77,33 @@ __device__ __forceinline__ float decayed(float gl, int d) {
   return d < 0 ? 0.f : e;
 }
 
+// The decay a^n of a state over n tokens.  Near 1 it is held as a^n - 1 and
+// added: a^n itself, rounded to float32, would be off by 2^-25 the same way at
+// every step, and a state that lives for 1 / (1 - a^n) steps by as many times
+// that (after 4096 chunks with decays of 1e-6 to 3.2e-4 a token 4e-5 to 9e-5).
+struct Decay {
+  float f;     // a^n, or a^n - 1
+  bool near;
+  __device__ __forceinline__ Decay(float ld, float n) {
+    const float x = ld * n;   // (NaN of -inf and no token: not near)
+    near = fabsf(x) <= 0.5f;
+    f = near ? expm1f(x) : ex2(log2_decay(ld) * n);
+    f = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f)));   // the same for a workgroup
+  }
+  template <int N>
+  __device__ __forceinline__ void apply(f32x4 (&m)[N][2]) const {
+    if (near) {
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[i / 2][i % 2][r] = fmaf(f, m[i / 2][i % 2][r], m[i / 2][i % 2][r]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i) m[i / 2][i % 2] *= f;
+    }
+  }
+};
+
 __device__ __forceinline__ int64_t tokens_of(const Sweep& a, int64_t b) {
   if (!a.lengths) return a.T;
   const int64_t n = a.lengths[b];
@@ -173,12 +200,6 @@ __device__ __forceinline__ int64_t segment_state(const SweepPlan& p, int sweep, 
   return ((sweep * p.pairs + pair) * p.segments + seg) * (KP * kVBlock * p.vblocks);
 }
 
-// Tokens of segment s of a sequence of `len`.
-__device__ __forceinline__ float tokens_in(const SweepPlan& p, int64_t len, int s) {
-  const int64_t left = len - (int64_t)s * p.seg_tokens;
-  return (float)(left < 0 ? 0 : left < p.seg_tokens ? left : p.seg_tokens);
-}
-
 // Up to so many segments, each adds up the earlier ones' states by itself;
 // more get theirs from the carry kernel.  Measured, us, so and with the kernel:
 // 4 segments (float32, 6 x 1023 tokens, V = 96) 59.7 / 64.0, 3 (float32
@@ -239,7 +260,7 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = wave >> 2, w = wave & 3;        // of the state: strip w, its key groups MJ * part..
   const int tb = part ? 3 - w : w;                 // of the outputs: tokens 16 tb.., values 32 OU part..
-  const float gl = log2_decay(a.log_decay[h]);
+  const float ld = a.log_decay[h], gl = log2_decay(ld);
 
   const int64_t len = tokens_of(a, b);
   const int64_t lo = (int64_t)seg * p.seg_tokens;
@@ -288,13 +309,15 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
     const f32x4* from = place(join ? p.segments - 1 : seg);
 #pragma unroll
     for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = from[64 * i];
-    if (join)
+    if (join && seg > 0) {
+      const Decay segment(ld, (float)p.seg_tokens);   // (what enters a segment behind the last token is not used)
       for (int s = 0; s < seg; ++s) {
-        const float d = ex2(gl * tokens_in(p, len, s));
+        segment.apply(M);
         from = place(s);
 #pragma unroll
-        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = M[i / 2][i % 2] * d + from[64 * i];
+        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] += from[64 * i];
       }
+    }
   }
 
   // ---- factors of whole chunks
@@ -318,6 +341,7 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
       }
   };
   update_factors(kChunk);
+  Decay whole(ld, kChunk);
 
   // ---- loads of a chunk of nt tokens (none: everything out of range)
   Raw8<BF> kr[KR], vr[VR], qr[SUMMARY ? 1 : NJ];
@@ -459,12 +483,11 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
 
     // ---- the state's update
     if (SUMMARY || c + 1 < nch || (a.s_out && last_seg)) {
-      if (nt < kChunk) update_factors(nt);
-      const float an = ex2(gl * nt);
-#pragma unroll
-      for (int J = 0; J < MJ; ++J)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) M[J][e] *= an;
+      if (nt < kChunk) {   // the last chunk
+        update_factors(nt);
+        whole = Decay(ld, nt);
+      }
+      whole.apply(M);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (32 * u < nt) {
@@ -525,7 +548,8 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
 }
 
 // The segments' own states, as the summaries left them, become the states
-// that enter the segments: M_0 = s_in, M_{s+1} = a^(tokens of s) M_s + U_s.
+// that enter the segments: M_0 = s_in, M_{s+1} = a^(a segment's tokens) M_s + U_s
+// (what enters a segment behind the last token is not used).
 // Bound by the latency of the chain's loads: 8 us for 16 heads x 16 segments
 // of 128 x 128 (34 MB).
 constexpr int kAhead = 8;
@@ -534,10 +558,9 @@ template <int KP>
 __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
   const Sweep& a = p.a[blockIdx.z];
   const int64_t pair = blockIdx.x, next = KP * kVBlock * p.vblocks / 4;
-  const int64_t len = tokens_of(a, pair / a.H);
-  const float gl = log2_decay(a.log_decay[pair % a.H]);
+  const Decay segment(a.log_decay[pair % a.H], (float)p.seg_tokens);
   f32x4* at = reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, blockIdx.z, pair, 0)) + blockIdx.y * kCarryThreads + threadIdx.x;
-  f32x4 m = at[(p.segments - 1) * next];
+  f32x4 m[1][2] = {{at[(p.segments - 1) * next], f32x4{0.f, 0.f, 0.f, 0.f}}};
   for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
     f32x4 u[kAhead];   // loaded together: the chain through m must not wait for memory
 #pragma unroll
@@ -547,8 +570,11 @@ __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
     for (int i = 0; i < kAhead; ++i) {
       const int s = s0 + i;
       if (s >= p.segments) break;
-      at[s * next] = m;
-      if (s + 1 < p.segments) m = m * ex2(gl * tokens_in(p, len, s)) + u[i];
+      at[s * next] = m[0][0];
+      if (s + 1 < p.segments) {
+        segment.apply(m);
+        m[0][0] += u[i];
+      }
     }
   }
 }
