@@ -77,31 +77,36 @@ __device__ __forceinline__ float decayed(float gl, int d) {
   return d < 0 ? 0.f : e;
 }
 
-// The decay a^n of a state over n tokens.  Near 1 it is held as a^n - 1 and
-// added: a^n itself, rounded to float32, would be off by 2^-25 the same way at
-// every step, and a state that lives for 1 / (1 - a^n) steps by as many times
-// that (after 4096 chunks with decays of 1e-6 to 3.2e-4 a token 4e-5 to 9e-5).
+// The decay a^n of a state over n tokens, in two float32 parts: rounded to one
+// it would be off by up to 2^-25 the same way at every step, and a state that
+// lives for 1 / (1 - a^n) steps by as many times that (after 4096 chunks with
+// decays of 1e-6 to 3.2e-4 a token 4e-5 to 9e-5).  Both parts are positive, so
+// that an infinite state stays what it is.
+//
+// A decay above 1 grows out of float32 over a long segment.  Then it is applied
+// as three factors that do not: a state of 0 stays 0, and any other one, of
+// 2^-149 or more, becomes infinite.
 struct Decay {
-  float f;     // a^n, or a^n - 1
-  bool near;
+  float hi, lo;   // or the third root and 0
+  bool large;
   __device__ __forceinline__ Decay(float ld, float n) {
-    const float x = ld * n;   // (NaN of -inf and no token: not near)
-    near = fabsf(x) <= 0.5f;
-    f = near ? expm1f(x) : ex2(log2_decay(ld) * n);
-    f = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f)));   // the same for a workgroup
+    const double e = (double)fmaxf(ld, -2839.f) * n;   // (-inf: exp(-2839) is 0 as well)
+    double a = exp(e);
+    large = a > 3.4028234663852886e38;
+    if (large) a = exp(fmin(e, 250.0) / 3.0);
+    float h = (float)a;
+    if (!large && (double)h >= a && h > 0.f) h = __uint_as_float(__float_as_uint(h) - 1);   // the next float32 below
+    hi = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(h)));   // the same for a workgroup
+    lo = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(large ? 0.f : (float)(a - (double)h))));
   }
-  template <int N>
-  __device__ __forceinline__ void apply(f32x4 (&m)[N][2]) const {
-    if (near) {
+  // over a chunk: a^64 is finite
+  __device__ __forceinline__ f32x4 chunk(f32x4 m) const {
 #pragma unroll
-      for (int i = 0; i < 2 * N; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[i / 2][i % 2][r] = fmaf(f, m[i / 2][i % 2][r], m[i / 2][i % 2][r]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2 * N; ++i) m[i / 2][i % 2] *= f;
-    }
+    for (int r = 0; r < 4; ++r) m[r] = fmaf(hi, m[r], lo * m[r]);   // (hi m rounded would drop lo m)
+    return m;
   }
+  // over a segment
+  __device__ __forceinline__ f32x4 segment(f32x4 m) const { return large ? m * hi * hi * hi : chunk(m); }
 };
 
 __device__ __forceinline__ int64_t tokens_of(const Sweep& a, int64_t b) {
@@ -267,6 +272,8 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
   const int64_t hi = lo + p.seg_tokens < len ? lo + p.seg_tokens : len;
   const int nch = lo < hi ? (int)((hi - lo + kChunk - 1) / kChunk) : 0;
 
+  const Decay whole(ld, kChunk), last(ld, (float)(hi - lo - (int64_t)(nch - 1) * kChunk));   // of a chunk, of the last one
+
   // ---- the entering state: rows c = 32J + 8g + 4e + r, column n of strip w
   f32x4 M[MJ][2];
   const int sn = v0 + 32 * (w >> 1) + 8 * (li >> 2) + 4 * (w & 1) + (li & 3);
@@ -310,12 +317,11 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
 #pragma unroll
     for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = from[64 * i];
     if (join && seg > 0) {
-      const Decay segment(ld, (float)p.seg_tokens);   // (what enters a segment behind the last token is not used)
+      const Decay decay(ld, (float)p.seg_tokens);   // (what enters a segment behind the last token is not used)
       for (int s = 0; s < seg; ++s) {
-        segment.apply(M);
         from = place(s);
 #pragma unroll
-        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] += from[64 * i];
+        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = decay.segment(M[i / 2][i % 2]) + from[64 * i];
       }
     }
   }
@@ -341,7 +347,6 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
       }
   };
   update_factors(kChunk);
-  Decay whole(ld, kChunk);
 
   // ---- loads of a chunk of nt tokens (none: everything out of range)
   Raw8<BF> kr[KR], vr[VR], qr[SUMMARY ? 1 : NJ];
@@ -483,11 +488,12 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
 
     // ---- the state's update
     if (SUMMARY || c + 1 < nch || (a.s_out && last_seg)) {
-      if (nt < kChunk) {   // the last chunk
-        update_factors(nt);
-        whole = Decay(ld, nt);
-      }
-      whole.apply(M);
+      if (nt < kChunk) update_factors(nt);
+      const Decay& decay = nt < kChunk ? last : whole;
+#pragma unroll
+      for (int J = 0; J < MJ; ++J)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) M[J][e] = decay.chunk(M[J][e]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (32 * u < nt) {
@@ -558,9 +564,9 @@ template <int KP>
 __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
   const Sweep& a = p.a[blockIdx.z];
   const int64_t pair = blockIdx.x, next = KP * kVBlock * p.vblocks / 4;
-  const Decay segment(a.log_decay[pair % a.H], (float)p.seg_tokens);
+  const Decay decay(a.log_decay[pair % a.H], (float)p.seg_tokens);
   f32x4* at = reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, blockIdx.z, pair, 0)) + blockIdx.y * kCarryThreads + threadIdx.x;
-  f32x4 m[1][2] = {{at[(p.segments - 1) * next], f32x4{0.f, 0.f, 0.f, 0.f}}};
+  f32x4 m = at[(p.segments - 1) * next];
   for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
     f32x4 u[kAhead];   // loaded together: the chain through m must not wait for memory
 #pragma unroll
@@ -570,11 +576,8 @@ __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
     for (int i = 0; i < kAhead; ++i) {
       const int s = s0 + i;
       if (s >= p.segments) break;
-      at[s * next] = m[0][0];
-      if (s + 1 < p.segments) {
-        segment.apply(m);
-        m[0][0] += u[i];
-      }
+      at[s * next] = m;
+      if (s + 1 < p.segments) m = decay.segment(m) + u[i];
     }
   }
 }
