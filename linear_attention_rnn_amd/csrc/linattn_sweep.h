@@ -90,7 +90,7 @@ struct Decay {
   float hi, lo;   // or the third root and 0
   bool large;
   __device__ __forceinline__ Decay(float ld, float n) {
-    const double e = (double)fmaxf(ld, -2839.f) * n;   // (-inf: exp(-2839) is 0 as well)
+    const double e = (double)ld * n;
     double a = exp(e);
     large = a > 3.4028234663852886e38;
     if (large) a = exp(fmin(e, 250.0) / 3.0);

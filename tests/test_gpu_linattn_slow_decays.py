@@ -74,3 +74,14 @@ def test_prompts_piece_by_piece(linattn, K, V, copies, dtype):  # noqa: F811
     n = T * pieces
     ref = f64(s0) * np.exp(n * f64(decay))[None, :, None, None]
     close(f"{copies * H} heads of {K} x {V}, {dtype}", s[:, :H], ref[:, :H], 3 * n / 64, n)
+
+
+@pytest.mark.parametrize("T", [4, 100, 1500])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decay_that_is_no_number(linattn, T, dtype):  # noqa: F811
+    """It spoils its head's state and no other's: also where nothing but the entering state is decayed."""
+    g = generator(4)
+    q, v = (normal(g, 1, T, 2, 64, dtype=TYPES[dtype]).cuda() for _ in range(2))
+    s0, decay = normal(g, 1, 2, 64, 64).cuda(), torch.tensor([-0.1, float("nan")]).cuda()
+    _, s = linattn.fwd(q, torch.zeros_like(q), v, decay, s_in=s0, want_state=True)
+    assert torch.isfinite(s[:, 0]).all() and torch.isnan(s[:, 1]).all()
