@@ -87,8 +87,10 @@ extern "C" {
  * with float32 accumulation.  With a float32 output every operand is carried
  * whole (three parts); with a bfloat16 output, weights between tokens and the
  * state as it meets the queries are rounded once to bfloat16, like the output.
- * The state itself is float32 throughout.  A NaN or infinity in k or v of a
- * token can reach all outputs of its chunk of 64 tokens and those after it.
+ * The state itself is float32 throughout.  A NaN or infinity in q reaches the
+ * outputs of its token, one in k those of its token and of later ones; in calls
+ * of more than 8 tokens one in v can also reach those of the up to 31 tokens
+ * before it in its chunk (their weight, 0, times it is NaN).
  */
 int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const void* q, const void* k, const void* v,
                 const float* log_decay, float scale, const int32_t* lengths, const float* s_in, void* o, float* s_out,
