@@ -87,7 +87,8 @@ extern "C" {
  * with float32 accumulation.  With a float32 output every operand is carried
  * whole (three parts); with a bfloat16 output, weights between tokens and the
  * state as it meets the queries are rounded once to bfloat16, like the output.
- * The state itself is float32 throughout.  A NaN or infinity in q reaches the
+ * The state itself is float32 throughout.  The outputs are the same bits
+ * whether or not s_out is asked for.  A NaN or infinity in q reaches the
  * outputs of its token, one in k those of its token and of later ones; in calls
  * of more than 8 tokens one in v can also reach those of the up to 31 tokens
  * before it in its chunk (their weight, 0, times it is NaN).

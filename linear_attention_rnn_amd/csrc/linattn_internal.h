@@ -62,7 +62,6 @@ hipError_t enqueue_sweeps(const Sweep* a, int n, void* workspace, hipStream_t st
 struct SweepPlan {
   Sweep a[kSweeps];
   int sweeps;
-  bool state_out;   // the call hands back a state
   float* ws;        // [sweeps][B H][segments] states of segments; null for one segment
   int segments;     // of each sequence
   int seg_tokens;   // tokens of a segment, a multiple of 64

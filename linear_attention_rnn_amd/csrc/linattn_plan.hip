@@ -164,7 +164,6 @@ SweepPlan plan(const Sweep* a, int n) {
   int blocks = 0;
   for (int i = 0; i < n; ++i) {
     p.a[i] = a[i];
-    p.state_out = p.state_out || a[i].s_out;
     const int vb = vblocks_of(a[i]);
     p.vblocks = std::max(p.vblocks, vb);
     blocks += vb;

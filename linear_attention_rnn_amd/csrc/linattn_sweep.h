@@ -29,9 +29,12 @@
 // carry what arises in between (scores times decays, the state as it meets
 // q): one where the output is bfloat16 too (each adds a rounding of the size
 // of the output's own, 2^-8, to the part of the output it carries), three
-// where it is float32.  UP parts carry the decayed values of the state's
-// update: two (2^-16) where the state ends in bfloat16 outputs alone, three
-// where it is handed back or read at float32.
+// where it is float32.  Two parts would leave the output's own rounding alone
+// (errors of 1.66e-3, one part 2.35e-3) and cost prompts of 256 heads 124 -> 132
+// us, prompts of 128 x 128 88 -> 106, gradients of 64 heads 108 -> 128.  The
+// decayed values of the state's update are always three parts, so that outputs
+// do not depend on whether the state is asked for (with two parts where it is
+// not: the prompts 124 and 82 us, the gradients 103).
 //
 // What bounds it.  256 heads of 4096 tokens and 64 channels in bfloat16: 126 to
 // 133 us, 4.0 to 4.3 TB/s, where a kernel that only loads and stores the same
@@ -231,7 +234,7 @@ constexpr int waves() {
   return KP == 128 && !BF ? 8 : 4;
 }
 
-template <int KP, bool BF, int MP, int UP, bool OBF, bool SUMMARY>
+template <int KP, bool BF, int MP, bool OBF, bool SUMMARY>
 __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
   constexpr int NW = waves<KP, BF>(), NT = 64 * NW, PARTS = NW / 4;
   constexpr int NI = BF ? 1 : 3;             // parts of an input operand
@@ -520,13 +523,13 @@ __global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) 
             if constexpr (NI == 3) f[j] += (float)vo.p[1][j] + (float)vo.p[2][j];
             f[j] *= uf[u][j];
           }
-          const Op<UP> vf = wkv6::split8<UP>(f);
+          const Op<3> vf = wkv6::split8<3>(f);
 #pragma unroll
           for (int J = 0; J < MJ; ++J)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int kj = MJ * part + J, kc = 4 * (kj & 1) + (li & 3);
-              M[J][e] = mma<NI, UP>(read_tr<NI>(Kp + (kj >> 1) * kPlane, KPL, at_col(kc, e, 0), at_col(kc, e, 4)), vf, M[J][e]);
+              M[J][e] = mma<NI, 3>(read_tr<NI>(Kp + (kj >> 1) * kPlane, KPL, at_col(kc, e, 0), at_col(kc, e, 4)), vf, M[J][e]);
             }
         }
       }
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
   }
 }
 
-template <int KP, bool BF, int MP, int UP, bool OBF>
+template <int KP, bool BF, int MP, bool OBF>
 hipError_t launch(const SweepPlan& of, hipStream_t s) {
   SweepPlan p = of;
   p.blocks = 0;
@@ -602,18 +605,18 @@ hipError_t launch(const SweepPlan& of, hipStream_t s) {
     SweepPlan q = p;
     q.items = p.pairs * (p.segments - 1);
     const unsigned parts = (unsigned)(KP * kVBlock * p.vblocks / (4 * kCarryThreads));
-    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, true>), grid(q.items), dim3((64 * waves<KP, BF>())), 0, s, q);
+    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, OBF, true>), grid(q.items), dim3((64 * waves<KP, BF>())), 0, s, q);
     if (p.segments > kJoin) hipLaunchKernelGGL(carry_kernel<KP>, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(kCarryThreads), 0, s, p);
   }
-  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, UP, OBF, false>), grid(p.items), dim3((64 * waves<KP, BF>())), 0, s, p);
+  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, OBF, false>), grid(p.items), dim3((64 * waves<KP, BF>())), 0, s, p);
   return hipGetLastError();
 }
 
 template <int KP>
 hipError_t launch_types(const SweepPlan& p, hipStream_t s) {
-  if (!p.a[0].bf16) return launch<KP, false, 3, 3, false>(p, s);
-  if (!p.a[0].out_bf16) return launch<KP, true, 3, 3, false>(p, s);
-  return p.state_out ? launch<KP, true, 1, 3, true>(p, s) : launch<KP, true, 1, 2, true>(p, s);
+  if (!p.a[0].bf16) return launch<KP, false, 3, false>(p, s);
+  if (!p.a[0].out_bf16) return launch<KP, true, 3, false>(p, s);
+  return launch<KP, true, 1, true>(p, s);
 }
 
 }  // namespace
