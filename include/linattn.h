@@ -151,7 +151,9 @@ size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
  *             itself (with the same strides), in place.
  *   positions NULL: token t has position start + t.  Else [B, T] int32,
  *             contiguous: its position is start + positions[b][t].
- *   start     added to every position.  Angles are formed in float64.
+ *   start     added to every position, from -2^52 to 2^52 (else UNSUPPORTED).
+ *             Angles are exact products, reduced before they are rounded: any
+ *             position is turned as precisely as a near one.
  *   freqs     R / 2 float64 values on the device: radians per position.
  *             Scaling for longer contexts is a matter of these values.
  *   inverse   nonzero: turn by the negative angle (the gradient of the

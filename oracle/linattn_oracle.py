@@ -64,14 +64,28 @@ def linattn_ref_backward(q, k, v, log_decay, do, scale=1.0, lengths=None, s_in=N
     return g
 
 
+# 1 / (2 pi) in units of 2^-256, from the first hundred decimals of pi
+_INVERSE_TURN = (10 ** 100 << 256) // (2 * int(
+    "3" "1415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679"))
+
+
+def rope_angles(positions, freqs):
+    """positions x freqs, less whole turns: radians in [0, 2 pi), [*, R / 2].  Products of whole positions and float64
+    frequencies are whole numbers of some 2^-n, multiplied by 1 / (2 pi) as such: exact to 2^-48 at any position."""
+    m, e = np.frexp(np.asarray(freqs, np.float64))
+    whole = np.ldexp(m, 53).astype(np.int64).astype(object)
+    turns = np.asarray(positions).astype(np.int64).astype(object)[..., None] * (whole * _INVERSE_TURN)
+    part = np.mod(turns >> (256 - 64 + 53 - e.astype(np.int64)).astype(object), 1 << 64)
+    return part.astype(np.float64) * (2 * np.pi / 2.0 ** 64)
+
+
 def rope_ref(x, positions, freqs, layout="half", inverse=False):
-    """x: [B, T, H, D]; positions: [B, T] whole numbers; freqs: [R / 2].  Angles
-    are reduced in extended precision, so far positions stay exact."""
+    """x: [B, T, H, D]; positions: [B, T] whole numbers; freqs: [R / 2].  Far
+    positions are exact."""
     x = np.array(x, np.float64)
     R = 2 * len(freqs)
-    turns = np.asarray(positions, np.float64)[:, :, None] * np.asarray(freqs, np.float64)   # the float64 angle
-    angle = np.remainder(turns.astype(np.longdouble), 2 * np.longdouble("3.14159265358979323846264338327950288"))
-    c, s = np.cos(angle).astype(np.float64)[:, :, None], np.sin(angle).astype(np.float64)[:, :, None]
+    angle = rope_angles(positions, freqs)
+    c, s = np.cos(angle)[:, :, None], np.sin(angle)[:, :, None]
     if inverse:
         s = -s
     i, j = (slice(0, R, 2), slice(1, R, 2)) if layout == "interleaved" else (slice(0, R // 2), slice(R // 2, R))
