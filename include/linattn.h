@@ -120,6 +120,8 @@ size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
  *             and dv.  An input with a distance of 0 gets one gradient row for
  *             each place it is used at; their sum is the caller's.
  *   T == 0    ds_in receives ds_out (or zero).
+ * Float32 gradients with K and V above 64 take up to 1398096 (batch, head)
+ * pairs (else UNSUPPORTED).
  * The decays are constants of the model and get no gradient.  Everything else
  * as linattn_fwd, the precision by grad_dtype.
  */

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "linattn_internal.h"
+#include "linattn_plan.h"
 #include "wkv6_host.h"
 
 namespace {
@@ -170,11 +171,16 @@ int check_sizes(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, int dtype
   if (K < 8 || V < 8 || K > LINATTN_MAX_HEAD || V > LINATTN_MAX_HEAD || K % 8 || V % 8)
     return unsupported("K and V must be multiples of 8 from 8 to 128");
   if (B == 0) return WKV6_OK;
-  // a launch holds fewer than 2^32 work-items: 256 for each (batch, head) pair,
-  // block of values (two) and sweep (three for the gradients)
   if (H > (1 << 21) || B > (1 << 21) / H)
     return unsupported("B * H exceeds the supported number of (batch, head) pairs (2^21)");
   if (T > INT_MAX - linattn::kChunk) return unsupported("T exceeds the supported range");
+  return WKV6_OK;
+}
+
+// A launch holds fewer than 2^32 work-items.
+int check_launches(const linattn::Sweep* a, int n) {
+  if (linattn::largest_launch(a, n) >= (int64_t(1) << 32))
+    return unsupported("B * H exceeds the (batch, head) pairs of these head sizes that a launch holds");
   return WKV6_OK;
 }
 
@@ -292,6 +298,7 @@ size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
   linattn::Sweep a = base_sweep(B, T, H, K, V, nullptr, &some, dtype, out_dtype);
   float any = 0.f;
   a.s_out = state_out ? &any : nullptr;
+  if (check_launches(&a, 1) != WKV6_OK) return 0;
   return linattn::sweep_workspace_bytes(&a, 1);
 } catch (...) {
   return 0;
@@ -305,6 +312,7 @@ int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   int st = check_sizes(B, T, H, K, V, dtype, out_dtype);
   if (st != WKV6_OK || B == 0) return st;
   linattn::Sweep a = base_sweep(B, T, H, K, V, log_decay, lengths, dtype, out_dtype);
+  if (T > 0 && (st = check_launches(&a, 1)) != WKV6_OK) return st;
   const int64_t sbytes = B * H * K * V * 4;
   Span s[9];
   int n = 0;
@@ -346,6 +354,7 @@ size_t linattn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
   float any = 0.f;
   const int32_t some = 0;
   bwd_sweeps(B, T, H, K, V, nullptr, 1.f, &some, nullptr, nullptr, state_grad ? &any : nullptr, none, dtype, grad_dtype, w);
+  if (check_launches(w, 3) != WKV6_OK) return 0;
   return linattn::sweep_workspace_bytes(w, 3);
 } catch (...) {
   return 0;
@@ -358,6 +367,10 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   set_error(WKV6_OK, "");
   int st = check_sizes(B, T, H, K, V, dtype, grad_dtype);
   if (st != WKV6_OK || B == 0) return st;
+  Tensor t[7] = {};
+  linattn::Sweep w[3];
+  bwd_sweeps(B, T, H, K, V, log_decay, scale, lengths, s_in, ds_out, ds_in, t, dtype, grad_dtype, w);
+  if (T > 0 && (st = check_launches(w, 3)) != WKV6_OK) return st;
   const int64_t sbytes = B * H * K * V * 4;
   Span s[12];
   int n = 0;
@@ -367,7 +380,6 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   s[n++] = flat("s_in", s_in, sbytes, false);
   s[n++] = flat("ds_out", ds_out, sbytes, false);
   s[n++] = flat("ds_in", ds_in, sbytes, true);
-  Tensor t[7] = {};
   if (T > 0) {
     const void* p[7] = {q, k, v, d_o, dq, dk, dv};
     const char* names[7] = {"q", "k", "v", "d_o", "dq", "dk", "dv"};
@@ -386,7 +398,6 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   if ((st = check_overlaps(s, n, allowed, 1)) != WKV6_OK) return st;
   const hipStream_t hs = static_cast<hipStream_t>(stream);
   if (T == 0) return finished(linattn::enqueue_state_copy(ds_out, ds_in, B * H * K * V, hs));
-  linattn::Sweep w[3];
   bwd_sweeps(B, T, H, K, V, log_decay, scale, lengths, s_in, ds_out, ds_in, t, dtype, grad_dtype, w);
   Workspace ws(hs);
   if ((st = ws.take(workspace, workspace_bytes, linattn::sweep_workspace_bytes(w, 3))) != WKV6_OK) return st;

@@ -15,6 +15,15 @@ constexpr int kChunk = 64;       // tokens of a chunk
 // 9.0; of 12 heads 3.7 / 6.6, 6.6 / 6.7, 8.6 / 6.7).
 constexpr int kStepTokens = 8;
 constexpr int kVBlock = 64;      // value channels one workgroup handles
+constexpr int kStepThreads = 256;   // of a workgroup of the token-by-token calls
+
+// Threads of a workgroup of the sweeps of up to KP (64 or 128) key channels.
+// LDS holds one float32 workgroup of more than 64 key channels at a time, so
+// that one gets a second set of four waves: the outputs' value channels and the
+// state's key channels are shared out between the two (gradients of K = 128, V =
+// 64, 2 x 777 tokens: 64.6 -> 61.6 us; prompts of 128 x 128: 100.5 -> 95.4).
+// With K = 64 two workgroups fit, and eight waves of one are slower (60 -> 74 us).
+constexpr int sweep_threads(int KP, bool bf16) { return KP == 128 && !bf16 ? 512 : 256; }
 
 // A [B, T, H, D] tensor: base and distances in elements (channels adjacent).
 struct Tensor {
@@ -70,6 +79,9 @@ struct SweepPlan {
   int64_t pairs;    // B H
   int64_t items;    // pairs * segments
 };
+// Workgroups of a launch over `items` items: eight of them side by side, see the
+// kernel.
+inline int64_t sweep_groups(const SweepPlan& p, int64_t items) { return (items + 7) / 8 * 8 * p.blocks; }
 hipError_t launch_sweeps64(const SweepPlan& p, hipStream_t s);    // K <= 64 in all sweeps
 hipError_t launch_sweeps128(const SweepPlan& p, hipStream_t s);
 

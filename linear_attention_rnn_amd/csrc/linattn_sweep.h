@@ -11,7 +11,7 @@
 //
 // All exponents are >= 0, so every factor is at most 1 for a decay a <= 1.
 //
-// A workgroup of four waves (eight: see waves()) runs one (batch item, head,
+// A workgroup of four waves (eight: see sweep_threads()) runs one (batch item, head,
 // block of 64 value channels, segment).  Wave w computes the outputs of tokens
 // 16w..16w+15 (all 64 channels, transposed: O^T[n][t]) and keeps the state's
 // columns of its strip of 16 value channels in registers.  MFMA operands chain
@@ -68,7 +68,6 @@ using wkv6::Op;
 using wkv6::Rsrc;
 using wkv6::swz;
 
-constexpr int NTH = 256;
 constexpr int kPlane = 64 * 64;   // a part of 64 rows of 64 channels
 
 // log2 of the decay, finite: the factor of any distance > 0 is 0 at -4096.
@@ -223,20 +222,9 @@ constexpr int occupancy() {
   return KP == 64 ? (BF && MP == 1 ? 3 : 2) : 2;
 }
 
-// Waves of a workgroup.  LDS holds one float32 workgroup of more than 64 key
-// channels at a time, so that one gets a second set of waves: the outputs'
-// value channels and the state's key channels are shared out between the two
-// (gradients of K = 128, V = 64, 2 x 777 tokens: 64.6 -> 61.6 us; prompts of
-// 128 x 128: 100.5 -> 95.4).  With K = 64 two workgroups fit, and eight waves
-// of one are slower (60 -> 74 us).
-template <int KP, bool BF>
-constexpr int waves() {
-  return KP == 128 && !BF ? 8 : 4;
-}
-
 template <int KP, bool BF, int MP, bool OBF, bool SUMMARY>
-__global__ __launch_bounds__((64 * waves<KP, BF>()), (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
-  constexpr int NW = waves<KP, BF>(), NT = 64 * NW, PARTS = NW / 4;
+__global__ __launch_bounds__(sweep_threads(KP, BF), (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
+  constexpr int NT = sweep_threads(KP, BF), PARTS = NT / 256;
   constexpr int NI = BF ? 1 : 3;             // parts of an input operand
   constexpr int ISZ = BF ? 2 : 4;
   constexpr int NJ = KP / 32;                // groups of 32 key channels
@@ -600,15 +588,15 @@ hipError_t launch(const SweepPlan& of, hipStream_t s) {
   SweepPlan p = of;
   p.blocks = 0;
   for (int i = 0; i < p.sweeps; ++i) p.blocks += vblocks_of(p.a[i]);
-  const auto grid = [&](int64_t items) { return dim3((unsigned)((items + 7) / 8 * 8 * p.blocks)); };
+  const auto grid = [&](int64_t items) { return dim3((unsigned)sweep_groups(p, items)); };
   if (p.segments > 1) {
     SweepPlan q = p;
     q.items = p.pairs * (p.segments - 1);
     const unsigned parts = (unsigned)(KP * kVBlock * p.vblocks / (4 * kCarryThreads));
-    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, OBF, true>), grid(q.items), dim3((64 * waves<KP, BF>())), 0, s, q);
+    hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, OBF, true>), grid(q.items), dim3(sweep_threads(KP, BF)), 0, s, q);
     if (p.segments > kJoin) hipLaunchKernelGGL(carry_kernel<KP>, dim3((unsigned)p.pairs, parts, p.sweeps), dim3(kCarryThreads), 0, s, p);
   }
-  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, OBF, false>), grid(p.items), dim3((64 * waves<KP, BF>())), 0, s, p);
+  hipLaunchKernelGGL((sweep_kernel<KP, BF, MP, OBF, false>), grid(p.items), dim3(sweep_threads(KP, BF)), 0, s, p);
   return hipGetLastError();
 }
 
