@@ -78,9 +78,10 @@ extern "C" {
  *             q, then of k, v and o; channels are always adjacent.  Each is
  *             >= 0 and a multiple of 16 bytes; a distance of 0 repeats an
  *             input (keys shared by all heads); the rows of o must not share
- *             elements.  Outputs and inputs may be slices of one buffer whose
- *             rows lie side by side (the same distances).  The distance of a
- *             dimension of one place does not matter.
+ *             elements.  Outputs and inputs may be slices of one buffer that
+ *             lie side by side (the same distances, but for those of heads that
+ *             differ in size: all q of a token, then all k, then all v).  The
+ *             distance of a dimension of one place does not matter.
  *   T == 0    s_out receives s_in (or zero).  B == 0: nothing is done.
  *
  * Precision: products run on matrix cores on bfloat16 parts of their operands

@@ -63,9 +63,10 @@ struct Dims {
 };
 
 // Whether rows of a (of `ra` bytes) and of b (of `rb`, starting `d` bytes
-// later) with the same distances share bytes, from dimension i on.
+// later) share bytes, from dimension i on: place by place as long as their
+// distances are the same, then by all that the remaining dimensions reach over.
 bool share_rows(const Dims& a, const Dims& b, int i, int64_t ra, int64_t rb, int64_t d) {
-  if (i == a.n) return d < ra && -d < rb;
+  if (i == a.n || i == b.n || a.step[i] != b.step[i]) return d < a.width(i, ra) && -d < b.width(i, rb);
   const int64_t s = a.step[i], wa = a.width(i + 1, ra), wb = b.width(i + 1, rb);
   if (s == 0 || wa > s || wb > s) return true;   // not told apart
   // b's place is m steps after a's: only a few m can meet
@@ -78,15 +79,12 @@ bool share_rows(const Dims& a, const Dims& b, int i, int64_t ra, int64_t rb, int
   return false;
 }
 
-// Whether two spans share bytes.  Disjoint ranges do not; rows of the same
-// distances (slices of one buffer, side by side) are told apart exactly;
-// everything else counts as sharing.
+// Whether two spans share bytes.  Disjoint ranges do not; slices of one buffer,
+// side by side, are told apart exactly, also where heads of different sizes lie
+// side by side within a token; everything else counts as sharing.
 bool share(const Span& a, const Span& b) {
   if (a.at + (uint64_t)a.bytes() <= b.at || b.at + (uint64_t)b.bytes() <= a.at) return false;
   const Dims da(a), db(b);
-  if (da.n != db.n) return true;
-  for (int i = 0; i < da.n; ++i)
-    if (da.step[i] != db.step[i]) return true;
   return share_rows(da, db, 0, a.row, b.row, (int64_t)(b.at - a.at));
 }
 
