@@ -12,10 +12,10 @@
  *   linattn_rms_norm_bwd  ... and its gradients
  *
  * Common to all.  Tensors are device memory of the caller, 16-byte aligned;
- * the library keeps no pointer after returning.  Calls are asynchronous on
- * `stream` (a hipStream_t; the current device must be the stream's), do not
- * synchronise the host and are thread-safe.  They return a WKV6_* status
- * (wkv6.h); on INVALID_ARG, UNSUPPORTED and MISALIGNED nothing is enqueued
+ * the library keeps no pointer after
+ * returning.  Calls are asynchronous on `stream` (a hipStream_t; the current
+ * device must be the stream's), do not synchronise the host and are
+ * thread-safe.  They return a WKV6_* status (wkv6.h); on INVALID_ARG, UNSUPPORTED and MISALIGNED nothing is enqueued
  * and wkv6_last_error says why.  Values are not checked: NaN and infinities
  * propagate.  Outputs must not overlap inputs or one another except where it
  * is said below.  Every result is bit-for-bit the same for the same call (no
@@ -81,7 +81,10 @@ extern "C" {
  *             elements.  Outputs and inputs may be slices of one buffer that
  *             lie side by side (the same distances, but for those of heads that
  *             differ in size: all q of a token, then all k, then all v).  The
- *             distance of a dimension of one place does not matter.
+ *             distance of a dimension of one place does not matter.  In calls
+ *             of more than 8 tokens (linattn_bwd: one) the token distance, also
+ *             that of contiguous tensors, is at most 33554288 bytes (else
+ *             UNSUPPORTED).
  *   T == 0    s_out receives s_in (or zero).  B == 0: nothing is done.
  *
  * Precision: products run on matrix cores on bfloat16 parts of their operands

@@ -132,9 +132,9 @@ int known_dtype(int dtype) {
 int size_of(int dtype) { return dtype == WKV6_DTYPE_BF16 ? 2 : 4; }
 
 // One tensor of a [B, T, H, D] call: its distances (3 values, or null:
-// contiguous), checked, and its span.
+// contiguous), checked, and its span.  `chunked`: rows are read a chunk at a time.
 int tensor(const char* name, const void* p, const int64_t* d, int64_t B, int64_t T, int64_t H, int64_t D, int dtype,
-           bool out, Tensor* t, Span* s) {
+           bool out, bool chunked, Tensor* t, Span* s) {
   int st = present(name, p);
   if (st != WKV6_OK) return st;
   const int z = size_of(dtype);
@@ -152,7 +152,7 @@ int tensor(const char* name, const void* p, const int64_t* d, int64_t B, int64_t
       return set_error(WKV6_ERR_MISALIGNED, std::string(name) + ": a stride is not a multiple of 16 bytes");
   }
   // a chunk's rows are addressed with 32-bit byte offsets
-  if (T > 1 && t->t > (INT_MAX - 8192) / (linattn::kChunk * 4))
+  if (chunked && T > 1 && t->t > (INT_MAX - 8192) / linattn::kChunk / z)
     return unsupported(std::string(name) + ": token stride exceeds the supported index range");
   *s = {name, reinterpret_cast<uintptr_t>(p), B, T, H, t->b * z, t->t * z, t->h * z, D * z, out};
   return WKV6_OK;
@@ -318,10 +318,11 @@ int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
   s[n++] = flat("s_in", s_in, sbytes, false);
   s[n++] = flat("s_out", s_out, sbytes, true);
   if (T > 0) {
-    if ((st = tensor("q", q, strides, B, T, H, K, dtype, false, &a.q, &s[n++])) != WKV6_OK ||
-        (st = tensor("k", k, strides ? strides + 3 : nullptr, B, T, H, K, dtype, false, &a.k, &s[n++])) != WKV6_OK ||
-        (st = tensor("v", v, strides ? strides + 6 : nullptr, B, T, H, V, dtype, false, &a.v, &s[n++])) != WKV6_OK ||
-        (st = tensor("o", o, strides ? strides + 9 : nullptr, B, T, H, V, out_dtype, true, &a.o, &s[n++])) != WKV6_OK ||
+    const bool chunked = !linattn::steps(&a, 1);
+    if ((st = tensor("q", q, strides, B, T, H, K, dtype, false, chunked, &a.q, &s[n++])) != WKV6_OK ||
+        (st = tensor("k", k, strides ? strides + 3 : nullptr, B, T, H, K, dtype, false, chunked, &a.k, &s[n++])) != WKV6_OK ||
+        (st = tensor("v", v, strides ? strides + 6 : nullptr, B, T, H, V, dtype, false, chunked, &a.v, &s[n++])) != WKV6_OK ||
+        (st = tensor("o", o, strides ? strides + 9 : nullptr, B, T, H, V, out_dtype, true, chunked, &a.o, &s[n++])) != WKV6_OK ||
         (st = present("log_decay", log_decay)) != WKV6_OK || (st = optional("lengths", lengths)) != WKV6_OK)
       return st;
     s[n++] = flat("log_decay", log_decay, H * 4, false);
@@ -384,7 +385,7 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
     const int64_t D[7] = {K, K, V, V, K, K, V};
     for (int i = 0; i < 7; ++i)
       if ((st = tensor(names[i], p[i], strides ? strides + 3 * i : nullptr, B, T, H, D[i], i < 4 ? dtype : grad_dtype,
-                       i >= 4, &t[i], &s[n++])) != WKV6_OK)
+                       i >= 4, true, &t[i], &s[n++])) != WKV6_OK)
         return st;
     if ((st = present("log_decay", log_decay)) != WKV6_OK || (st = optional("lengths", lengths)) != WKV6_OK) return st;
     s[n++] = flat("log_decay", log_decay, H * 4, false);
@@ -429,8 +430,8 @@ int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const vo
       s[n++] = flat(names[i], nullptr, 0, false);
       continue;
     }
-    if ((st = tensor(names[i], p[i], strides ? strides + 3 * i : nullptr, B, T, H, D, dtype, i >= 2, to[i], &s[n++])) !=
-        WKV6_OK)
+    if ((st = tensor(names[i], p[i], strides ? strides + 3 * i : nullptr, B, T, H, D, dtype, i >= 2, false, to[i],
+                     &s[n++])) != WKV6_OK)
       return st;
   }
   if ((st = present("freqs", freqs)) != WKV6_OK || (st = optional("positions", positions)) != WKV6_OK) return st;
