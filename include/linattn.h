@@ -11,8 +11,8 @@
  *   linattn_rms_norm_q8   ... with an 8-bit output and its scales,
  *   linattn_rms_norm_bwd  ... and its gradients
  *
- * Common to all.  Tensors are device memory of the caller, 16-byte aligned;
- * the library keeps no pointer after
+ * Common to all.  Tensors are device memory of the caller, 16-byte aligned
+ * (log_decay and positions: 4-byte); the library keeps no pointer after
  * returning.  Calls are asynchronous on `stream` (a hipStream_t; the current
  * device must be the stream's), do not synchronise the host and are
  * thread-safe.  They return a WKV6_* status (wkv6.h); on INVALID_ARG, UNSUPPORTED and MISALIGNED nothing is enqueued

@@ -116,14 +116,15 @@ int check_overlaps(const Span* s, int n, const int (*allowed)[2], int na) {
 // list of pools): no exception leaves it.
 int no_memory() { return WKV6_ERR_HIP; }
 
-int present(const char* name, const void* p) {
+// (tables that are read value by value may start at any of them: `align`)
+int present(const char* name, const void* p, int align = 16) {
   if (!p) return invalid(std::string("null pointer: ") + name);
-  if (reinterpret_cast<uintptr_t>(p) % 16)
-    return set_error(WKV6_ERR_MISALIGNED, std::string("pointer not 16-byte aligned: ") + name);
+  if (reinterpret_cast<uintptr_t>(p) % align)
+    return set_error(WKV6_ERR_MISALIGNED, "pointer not " + std::to_string(align) + "-byte aligned: " + name);
   return WKV6_OK;
 }
 
-int optional(const char* name, const void* p) { return p ? present(name, p) : WKV6_OK; }
+int optional(const char* name, const void* p, int align = 16) { return p ? present(name, p, align) : WKV6_OK; }
 
 int known_dtype(int dtype) {
   return dtype == WKV6_DTYPE_F32 || dtype == WKV6_DTYPE_BF16 ? WKV6_OK : invalid("unknown dtype");
@@ -323,7 +324,7 @@ int linattn_fwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
         (st = tensor("k", k, strides ? strides + 3 : nullptr, B, T, H, K, dtype, false, chunked, &a.k, &s[n++])) != WKV6_OK ||
         (st = tensor("v", v, strides ? strides + 6 : nullptr, B, T, H, V, dtype, false, chunked, &a.v, &s[n++])) != WKV6_OK ||
         (st = tensor("o", o, strides ? strides + 9 : nullptr, B, T, H, V, out_dtype, true, chunked, &a.o, &s[n++])) != WKV6_OK ||
-        (st = present("log_decay", log_decay)) != WKV6_OK || (st = optional("lengths", lengths)) != WKV6_OK)
+        (st = present("log_decay", log_decay, 4)) != WKV6_OK || (st = optional("lengths", lengths)) != WKV6_OK)
       return st;
     s[n++] = flat("log_decay", log_decay, H * 4, false);
     s[n++] = flat("lengths", lengths, B * 4, false);
@@ -387,7 +388,7 @@ int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const voi
       if ((st = tensor(names[i], p[i], strides ? strides + 3 * i : nullptr, B, T, H, D[i], i < 4 ? dtype : grad_dtype,
                        i >= 4, true, &t[i], &s[n++])) != WKV6_OK)
         return st;
-    if ((st = present("log_decay", log_decay)) != WKV6_OK || (st = optional("lengths", lengths)) != WKV6_OK) return st;
+    if ((st = present("log_decay", log_decay, 4)) != WKV6_OK || (st = optional("lengths", lengths)) != WKV6_OK) return st;
     s[n++] = flat("log_decay", log_decay, H * 4, false);
     s[n++] = flat("lengths", lengths, B * 4, false);
   } else if (!ds_in) {
@@ -434,7 +435,7 @@ int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const vo
                      &s[n++])) != WKV6_OK)
       return st;
   }
-  if ((st = present("freqs", freqs)) != WKV6_OK || (st = optional("positions", positions)) != WKV6_OK) return st;
+  if ((st = present("freqs", freqs)) != WKV6_OK || (st = optional("positions", positions, 4)) != WKV6_OK) return st;
   s[n++] = flat("positions", positions, B * T * 4, false);
   s[n++] = flat("freqs", freqs, R / 2 * 8, false);
   const int allowed[2][2] = {{2, 0}, {3, 1}};

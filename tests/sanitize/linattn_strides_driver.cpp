@@ -1,6 +1,6 @@
 // Distances between tokens (linattn.h): as far apart as the kernels reach, and
 // refused beyond, in bytes of the tensor's own type; single tokens and rotary
-// positions at any distance.
+// positions at any distance; log_decay and positions at any element of a table.
 // Built with the host sanitizers; the kernel side is stubs.  Exits 0 when all
 // of it holds.
 #include <cstdint>
@@ -66,6 +66,13 @@ int main() {
   // an out_dtype of its own: o's distance counts in its own bytes
   int64_t s[12] = {0, 64, 64, 0, 64, 64, 0, 64, 64, 0, most / 4 + 4, 64};
   EXPECT(fwd(9, 1, 1, 1, s) == WKV6_OK && fwd(9, 1, 1, 0, s) == WKV6_ERR_UNSUPPORTED);
+  // one layer's row of a table, one sequence's of the positions
+  for (int i = 1; i < 4; ++i) {
+    EXPECT(fwd(9, 3, 1, 1, nullptr, F(3) + i) == WKV6_OK);
+    EXPECT(rope(3, 1, 1, nullptr, reinterpret_cast<int32_t*>(P(6)) + i) == WKV6_OK);
+    EXPECT(fwd(9, 3, 1, 1, nullptr, reinterpret_cast<float*>(P(3) + i)) == WKV6_ERR_MISALIGNED);
+    EXPECT(rope(3, 1, 1, nullptr, reinterpret_cast<int32_t*>(P(6) + i)) == WKV6_ERR_MISALIGNED);
+  }
   if (failures) return 1;
   std::puts("all distances hold");
   return 0;

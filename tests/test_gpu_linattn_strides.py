@@ -1,5 +1,6 @@
 """Token rows up to 33.5 MB apart, and any distance for single tokens and rotary
-positions.  Bit for bit the calls on packed tensors."""
+positions; one layer's row of a table of decays.  Bit for bit the calls on
+packed tensors."""
 import pytest
 import torch
 
@@ -41,3 +42,16 @@ def test_rotary_positions_far_apart(linattn):  # noqa: F811
     want, _ = linattn.rope(q, None, freqs, start=5)
     linattn.rope(x, None, freqs, start=5, q_out=x)
     assert bits(x, want)
+
+
+def test_rows_of_tables(linattn):  # noqa: F811
+    g = generator(2)
+    H = 3
+    decays = -0.1 * torch.arange(1, 13, dtype=torch.float32, device="cuda").view(4, H)
+    for T in (1, 100):
+        q, k, v = (normal(g, 4, T, H, 64, dtype=torch.bfloat16).cuda() for _ in range(3))
+        positions = torch.randint(0, 9999, (4, T), generator=g, dtype=torch.int32).cuda()
+        freqs = linattn.rope_freqs(64)
+        for i in range(4):
+            assert bits(linattn.fwd(q, k, v, decays[i])[0], linattn.fwd(q, k, v, decays[i].clone())[0])
+            assert bits(linattn.rope(q[i:], None, freqs, positions[i:])[0], linattn.rope(q, None, freqs, positions)[0][i:])

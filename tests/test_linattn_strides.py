@@ -1,4 +1,5 @@
-"""Distances between rows at the limits of what the kernels reach: the argument checks of linattn.h on the host, with kernels
+"""Distances between rows at the limits of what the kernels reach, and tables that
+start at any element: the argument checks of linattn.h on the host, with kernels
 replaced by stubs."""
 import os
 import shutil
