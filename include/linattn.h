@@ -127,7 +127,9 @@ size_t linattn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t K, i
  * Float32 gradients with K and V above 64 take up to 1398096 (batch, head)
  * pairs (else UNSUPPORTED).
  * The decays are constants of the model and get no gradient.  Everything else
- * as linattn_fwd, the precision by grad_dtype.
+ * as linattn_fwd, the precision by grad_dtype.  What is not finite in k can also
+ * reach dq of the up to 31 tokens before its own; in q dk, and in d_o dv, of the
+ * up to 31 behind (these two run from the last token to the first).
  */
 int linattn_bwd(int64_t B, int64_t T, int64_t H, int64_t K, int64_t V, const void* q, const void* k, const void* v,
                 const float* log_decay, float scale, const int32_t* lengths, const float* s_in, const void* d_o,

@@ -231,7 +231,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(Norm a) {
 // ---- gradients.  A workgroup walks over rows a grid apart and keeps its
 // columns' sums of dy h r in registers; the workgroups' sums go to the
 // workspace and are added up in the order of the workgroups.  16384 rows of
-// 1024 columns in bfloat16: 28 us, 4.8 TB/s, of which the sums 3 us (without the
+// 1024 columns in bfloat16: 28 us, 4.7 TB/s, of which the sums 4 us (without the
 // next row's loads in flight 45 us); 2048 columns of float32 77 us, 5.2 TB/s.
 template <int TPR, int NV, bool BF>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd a, float* part) {

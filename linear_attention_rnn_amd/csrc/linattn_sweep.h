@@ -11,8 +11,8 @@
 //
 // All exponents are >= 0, so every factor is at most 1 for a decay a <= 1.
 //
-// A workgroup of four waves (eight: see sweep_threads()) runs one (batch item, head,
-// block of 64 value channels, segment).  Wave w computes the outputs of tokens
+// A workgroup of four waves (eight: see sweep_threads()) runs one (batch item,
+// head, block of 64 value channels, segment).  Wave w computes the outputs of tokens
 // 16w..16w+15 (all 64 channels, transposed: O^T[n][t]) and keeps the state's
 // columns of its strip of 16 value channels in registers.  MFMA operands chain
 // without a detour: scores come out as K Q^T tiles whose accumulator lanes are,
@@ -214,16 +214,17 @@ __device__ __forceinline__ int64_t segment_state(const SweepPlan& p, int sweep, 
 // 79.8 / 73.7, 128 40.3 / 31.0.
 constexpr int kJoin = 8;
 
-// Waves a SIMD that the registers leave room for: three of the bfloat16 sweeps
-// of 64 key channels (166 registers; a fourth would spill), else two, which LDS
-// allows as well (float32: 74 KB a workgroup of 64 key channels, 123 KB of 128).
-template <int KP, bool BF, int MP>
+// Waves a SIMD: three of the bfloat16 sweeps of 64 key channels (168 registers,
+// 24 or 41 KB of LDS a workgroup; a fourth would spill), else two, by registers
+// (bfloat16 of 128 key channels: 218) or LDS (float32: 74 KB of 64 key channels;
+// 123 KB of 128, eight waves of one workgroup).
+template <int KP, bool BF>
 constexpr int occupancy() {
-  return KP == 64 ? (BF && MP == 1 ? 3 : 2) : 2;
+  return KP == 64 && BF ? 3 : 2;
 }
 
 template <int KP, bool BF, int MP, bool OBF, bool SUMMARY>
-__global__ __launch_bounds__(sweep_threads(KP, BF), (occupancy<KP, BF, MP>())) void sweep_kernel(SweepPlan p) {
+__global__ __launch_bounds__(sweep_threads(KP, BF), (occupancy<KP, BF>())) void sweep_kernel(SweepPlan p) {
   constexpr int NT = sweep_threads(KP, BF), PARTS = NT / 256;
   constexpr int NI = BF ? 1 : 3;             // parts of an input operand
   constexpr int ISZ = BF ? 2 : 4;

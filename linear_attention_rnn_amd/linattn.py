@@ -358,7 +358,9 @@ def retention(q, k, v, log_decay, freqs, positions=None, start: int = 0, layout:
 def retention_bwd(q, k, v, log_decay, do, freqs, positions=None, start: int = 0, layout: str = "half",
                   **bwd_arguments) -> dict:
     """Gradients of retention(...): those of bwd at the turned q and k, turned
-    back.  Other arguments as bwd."""
+    back.  Other arguments as bwd.  bfloat16 gradients of q and k are rounded
+    before they are turned and again after (float32 ones, the default, once
+    each at 2^-24); keys that heads share are turned for each of them."""
     stream = bwd_arguments.get("stream")
     q, k = _turned(q, k, freqs, positions, start, layout, stream)
     g = bwd(q, k, v, log_decay, do, **bwd_arguments)
