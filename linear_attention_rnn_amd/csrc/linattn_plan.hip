@@ -13,7 +13,7 @@ constexpr int NTH = kStepThreads;
 // with the state's 64 columns of a block in registers: thread (x, y) holds
 // rows y, y + 16, .. of columns 4x..4x+3.  Bound by the state's bytes, read
 // and written once as whole 256-byte rows: one token of 256 x 32 heads of 64 x
-// 64, 50 us, 5.4 TB/s; of 12 heads 4 us, a launch.
+// 64, 51 us, 5.4 TB/s; of 12 heads 4 us, a launch.
 //
 // The decay is carried in two parts, a = hi + lo: rounded to float32 it would
 // be off the same way at every token, and a state that lives for 1 / (1 - a)

@@ -36,19 +36,14 @@
 // do not depend on whether the state is asked for (with two parts where it is
 // not: the prompts 124 and 82 us, the gradients 103).
 //
-// What bounds it.  256 heads of 4096 tokens and 64 channels in bfloat16: 126 to
-// 133 us, 4.0 to 4.3 TB/s, where a kernel that only loads and stores the same
-// 128-byte pieces 4 KiB apart takes 118 us; with each head's rows adjacent 105
-// us, 5.1 TB/s, the rate of a copy.  The gradients of the same 320 us for 1.41
-// GB (the sweeps run both ways, so q, k, v and d_o come from memory nearly
-// twice), 4.4 TB/s.  With fewer workgroups than CUs a chunk's own chain of
-// steps sets the time, 3300 cycles of K = V = 64 and 5300 of K = 128 (float32:
-// three to four times that, for six products of parts).  Measured without gain:
-// blocks of 32 value channels, chunks of 128 tokens with eight waves (gradients
-// of 64 heads: 103 -> 113 us), eight waves of bfloat16 heads (103 -> 110),
-// waves with roles of their own for outputs and state (126 -> 148), LDS places
-// without any bank conflict (no change), loads two chunks ahead, streaming
-// loads and stores (126 -> 139).
+// What bounds it.  256 heads of 4096 tokens and 64 channels in bfloat16: 125 us,
+// 4.3 TB/s, where a kernel that only loads and stores the same 128-byte pieces 4
+// KiB apart takes 118 us; with each head's rows adjacent 110 us, 4.9 TB/s (a
+// copy: 5.1).  The gradients of the same 324 us for 1.41 GB (the sweeps run both
+// ways, so q, k, v and d_o come from memory nearly twice), 4.4 TB/s.  With fewer
+// workgroups than CUs a chunk's own chain of steps sets the time, 3450 cycles of
+// K = V = 64 and 5400 of K = 128 (float32: three to four times that, for six
+// products of parts).
 #pragma once
 
 #include "linattn_internal.h"
