@@ -80,9 +80,10 @@ __device__ __forceinline__ float decayed(float gl, int d) {
 // decays of 1e-6 to 3.2e-4 a token 4e-5 to 9e-5).  Both parts are positive, so
 // that an infinite state stays what it is.
 //
-// A decay above 1 grows out of float32 over a long segment.  Then it is applied
-// as three factors that do not: a state of 0 stays 0, and any other one, of
-// 2^-149 or more, becomes infinite.
+// SEGMENT: a decay above 1 grows out of float32 over a long segment (over a chunk
+// it must not).  Then it is applied as three factors that do not: a state of 0
+// stays 0, and any other one, of 2^-149 or more, becomes infinite.
+template <bool SEGMENT>
 struct Decay {
   float hi, lo;   // or the third root and 0
   bool large;
@@ -90,20 +91,18 @@ struct Decay {
     const double e = (double)ld * n;
     double a = exp(e);
     large = a > 3.4028234663852886e38;
-    if (large) a = exp(fmin(e, 250.0) / 3.0);
+    if (SEGMENT && large) a = exp(fmin(e, 250.0) / 3.0);
     float h = (float)a;
     if (!large && (double)h >= a && h > 0.f) h = __uint_as_float(__float_as_uint(h) - 1);   // the next float32 below
     hi = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(h)));   // the same for a workgroup
     lo = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(large ? 0.f : (float)(a - (double)h))));
   }
-  // over a chunk: a^64 is finite
-  __device__ __forceinline__ f32x4 chunk(f32x4 m) const {
+  __device__ __forceinline__ f32x4 operator()(f32x4 m) const {
+    if (SEGMENT && large) return m * hi * hi * hi;
 #pragma unroll
     for (int r = 0; r < 4; ++r) m[r] = fmaf(hi, m[r], lo * m[r]);   // (hi m rounded would drop lo m)
     return m;
   }
-  // over a segment
-  __device__ __forceinline__ f32x4 segment(f32x4 m) const { return large ? m * hi * hi * hi : chunk(m); }
 };
 
 __device__ __forceinline__ int64_t tokens_of(const Sweep& a, int64_t b) {
@@ -259,7 +258,7 @@ __global__ __launch_bounds__(sweep_threads(KP, BF), (occupancy<KP, BF>())) void 
   const int64_t hi = lo + p.seg_tokens < len ? lo + p.seg_tokens : len;
   const int nch = lo < hi ? (int)((hi - lo + kChunk - 1) / kChunk) : 0;
 
-  const Decay whole(ld, kChunk), last(ld, (float)(hi - lo - (int64_t)(nch - 1) * kChunk));   // of a chunk, of the last one
+  const Decay<false> whole(ld, kChunk), last(ld, (float)(hi - lo - (int64_t)(nch - 1) * kChunk));   // of a chunk, of the last one
 
   // ---- the entering state: rows c = 32J + 8g + 4e + r, column n of strip w
   f32x4 M[MJ][2];
@@ -304,11 +303,11 @@ __global__ __launch_bounds__(sweep_threads(KP, BF), (occupancy<KP, BF>())) void 
 #pragma unroll
     for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = from[64 * i];
     if (join && seg > 0) {
-      const Decay decay(ld, (float)p.seg_tokens);   // (what enters a segment behind the last token is not used)
+      const Decay<true> decay(ld, (float)p.seg_tokens);   // (what enters a segment behind the last token is not used)
       for (int s = 0; s < seg; ++s) {
         from = place(s);
 #pragma unroll
-        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = decay.segment(M[i / 2][i % 2]) + from[64 * i];
+        for (int i = 0; i < 2 * MJ; ++i) M[i / 2][i % 2] = decay(M[i / 2][i % 2]) + from[64 * i];
       }
     }
   }
@@ -486,11 +485,11 @@ __global__ __launch_bounds__(sweep_threads(KP, BF), (occupancy<KP, BF>())) void 
     // ---- the state's update
     if (SUMMARY || c + 1 < nch || (a.s_out && last_seg)) {
       if (nt < kChunk) update_factors(nt);
-      const Decay& decay = nt < kChunk ? last : whole;
+      const Decay<false>& decay = nt < kChunk ? last : whole;
 #pragma unroll
       for (int J = 0; J < MJ; ++J)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) M[J][e] = decay.chunk(M[J][e]);
+        for (int e = 0; e < 2; ++e) M[J][e] = decay(M[J][e]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (32 * u < nt) {
@@ -561,7 +560,7 @@ template <int KP>
 __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
   const Sweep& a = p.a[blockIdx.z];
   const int64_t pair = blockIdx.x, next = KP * kVBlock * p.vblocks / 4;
-  const Decay decay(a.log_decay[pair % a.H], (float)p.seg_tokens);
+  const Decay<true> decay(a.log_decay[pair % a.H], (float)p.seg_tokens);
   f32x4* at = reinterpret_cast<f32x4*>(p.ws + segment_state<KP>(p, blockIdx.z, pair, 0)) + blockIdx.y * kCarryThreads + threadIdx.x;
   f32x4 m = at[(p.segments - 1) * next];
   for (int s0 = 0; s0 < p.segments; s0 += kAhead) {
@@ -574,7 +573,7 @@ __global__ __launch_bounds__(kCarryThreads) void carry_kernel(SweepPlan p) {
       const int s = s0 + i;
       if (s >= p.segments) break;
       at[s * next] = m;
-      if (s + 1 < p.segments) m = decay.segment(m) + u[i];
+      if (s + 1 < p.segments) m = decay(m) + u[i];
     }
   }
 }

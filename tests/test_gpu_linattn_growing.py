@@ -71,3 +71,26 @@ def test_gradients_of_the_first_tokens_alone(linattn, K, V, dtype, grad):  # noq
         check("d" + n, got[n][:, :ACTIVE], ref[n], size[n], max(K, V), grad == "bf16")
         assert torch.all(got[n][:, ACTIVE:] == 0)
     check("ds_in", got["s_in"], ref["s_in"], size["s_in"], max(K, V), False)
+
+
+@pytest.mark.parametrize("copies", [100, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_overflow_shows(linattn, copies, dtype):  # noqa: F811
+    """Past the documented range (a^64 is infinite) a state is infinite or NaN, never a wrong number: in one run of chunks
+    and in segments."""
+    g = generator(9)
+    q, k, v = (normal(g, 1, 1500, 2, 64, dtype=TYPES[dtype]).cuda().repeat(1, 1, copies, 1) for _ in range(3))
+    decay = torch.tensor([2.0, 1.5] * copies, device="cuda")
+    assert (linattn.fwd_workspace_bytes(1, 1500, 2 * copies, 64, 64, TYPES[dtype], state_out=True) > 0) == (copies == 1)
+    o, S = linattn.fwd(q, k, v, decay, want_state=True)
+    assert not torch.isfinite(S).any() and not torch.isfinite(o[:, 200:]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_overflow_of_the_entering_state_shows(linattn, dtype):  # noqa: F811
+    """a^63 is finite and a^64 is not; nothing but the entering state grows."""
+    g = generator(10)
+    q, v = (normal(g, 1, 70, 1, 64, dtype=TYPES[dtype]).cuda() for _ in range(2))
+    s0 = 1 + normal(g, 1, 1, 64, 64).abs().cuda()
+    _, S = linattn.fwd(q, torch.zeros_like(q), v, torch.tensor([1.4], device="cuda"), s_in=s0, want_state=True)
+    assert not torch.isfinite(S).any()
