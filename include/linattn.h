@@ -179,7 +179,9 @@ int linattn_rope(int64_t B, int64_t T, int64_t H, int64_t D, int64_t R, const vo
  *     h = x + residual  (rounded to `dtype`);   y = h / sqrt(mean(h^2) + eps) * weight
  *
  * with the mean over the C columns of each row.  The norm is that of h as it
- * is stored, so that linattn_rms_norm_bwd sees the same values.
+ * is stored, so that linattn_rms_norm_bwd sees the same values.  Squares are
+ * added up in float32: rows whose sum of squares leaves its range, 2^128, give
+ * y = 0.
  *
  *   rows, C   C is a multiple of 8 up to LINATTN_MAX_COLUMNS; at most 2^25
  *             rows, or 2^21 of more than 1024 columns
