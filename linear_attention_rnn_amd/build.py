@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libwkv6.so")
 SOURCES = ["wkv6_kernels.hip", "wkv6_backward.hip", "wkv6_backward_chunked.hip", "wkv4_kernels.hip", "wkv6_groupnorm.hip", "wkv6_api.cpp",
-           "linattn_plan.hip", "linattn_sweep64.hip", "linattn_sweep128.hip", "linattn_rope.hip", "linattn_norm.hip", "linattn_api.cpp"]
+           "linattn_plan.hip", "linattn_sweep64.hip", "linattn_sweep128.hip", "linattn_rope.hip", "linattn_norm.hip", "linattn_api.cpp",
+           "ssm_conv.hip", "ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_norm.hip", "ssm_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,203 @@
+// The selective scan over blocks of tokens, shared by the forward kernel and
+// the gradients.  Per channel d and state n, with the step delta_t = softplus(dt_t
+// + bias):
+//
+//   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,   y_t = sum_n C_t h_t
+//
+// A wave holds one channel over a block of 16 R tokens: lane (q, l) = (lane /
+// 16, lane % 16) has the R tokens from l R on and the NL states from q NL on, so
+// that four lanes hold a token's states.  B and C of its tokens and states are the
+// same for every channel of a group and stay in registers while the wave goes
+// through its channels.  Per channel:
+//   1. decays e = exp(delta A) and inputs u = delta x B of the lane, its own
+//      state H from zero, its decay P = exp(A sum delta);
+//   2. the 16 lanes' (P, H) are combined in four doubling steps within a row of
+//      16 lanes, and the state at the block's start joins them, decayed by exp(A
+//      (sum of all steps up to there)): one rounding for a block, where the product of a
+//      token's decays would be off the same way at every token;
+//   3. the lane goes through its tokens again from the state in front of them.
+// Decays and inputs stay in registers between 1 and 3: 2 more instructions for
+// each token and state than a walk over the tokens, and the scan's, for 16 times
+// as many lanes.  Bound by the vector instructions: per token and state about 10
+// (an exp counts two), and about 70 per token for softplus and gate.
+#pragma once
+
+#include "ssm_device.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kLanes = 16;   // lanes over a block's tokens
+
+// Sizes of one instance: NL states a lane, R tokens a lane, DW channels and NW
+// waves a workgroup.
+template <int NL_, int R_, int DW_, int NW_>
+struct Shape {
+  static constexpr int NL = NL_, R = R_, DW = DW_, NW = NW_;
+  static constexpr int N = 4 * NL, TB = kLanes * R, NT = 64 * NW;
+  static constexpr int V = R < 4 ? R : 4;       // tokens of one access to a channel's row
+  static constexpr int LD = TB + 4;             // floats of a channel's row
+  static constexpr int PIECES = TB * (DW / 8);  // of 8 channels of a token
+  static constexpr int TURNS = (PIECES + NT - 1) / NT;
+  static constexpr int BPIECES = TB * (N / 8);  // of 8 states of a token
+  static constexpr int BTURNS = (BPIECES + NT - 1) / NT;
+  // Where token t of a block lies in a channel's row: the lanes' first V tokens
+  // side by side, then their next, so that a wave reads whole lines.
+  static __device__ __forceinline__ int at(int t) {
+    if constexpr (R <= 4)
+      return t;
+    else
+      return t % R / 4 * (4 * kLanes) + t / R * 4 + t % 4;
+  }
+  // Where B and C of token t, states from n on, lie: lanes side by side.
+  static __device__ __forceinline__ int at(int t, int n) { return ((n / NL * R + t % R) * kLanes + t / R) * NL + n % NL; }
+};
+
+// A lane's tokens of a channel's row.
+template <class S>
+__device__ __forceinline__ void get_tokens(const float* row, int l, float (&x)[S::R]) {
+#pragma unroll
+  for (int i = 0; i < S::R; i += S::V) {
+    const float* p = row + i / 4 * (4 * kLanes) + l * S::V;
+    if constexpr (S::V == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p);
+      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(p);
+      x[i] = f.x, x[i + 1] = f.y;
+    }
+  }
+}
+
+template <int NL>
+__device__ __forceinline__ void get_states(const float* p, float (&x)[NL]) {
+  if constexpr (NL == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    x[0] = f.x, x[1] = f.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+    }
+  }
+}
+template <int NL>
+__device__ __forceinline__ void put_states(float* p, const float (&x)[NL]) {
+  if constexpr (NL == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  }
+}
+
+// Sums over the four lanes of a token's states, put into the lane's channel row
+// at its tokens.  The lane exchanges add up two tokens at a time.
+template <class S>
+__device__ __forceinline__ void put_sums(float* row, int q, int l, const float (&y)[S::R]) {
+  if constexpr (S::R == 2) {
+    const float w = halves_sum(y[0], y[1]);
+    const float z = rows16_sum(w, w);   // rows 0, 1: the first token, 2, 3: the second
+    if (q % 2 == 0) row[2 * l + q / 2] = z;
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::R; i += 4) {
+      const float z = rows16_sum(halves_sum(y[i], y[i + 1]), halves_sum(y[i + 2], y[i + 3]));
+      // rows 0 to 3 hold tokens 0, 2, 1, 3
+      row[i / 4 * (4 * kLanes) + 4 * l + (q % 2 * 2 + q / 2)] = z;
+    }
+  }
+}
+
+// A channel's decays and inputs of a lane, and the state in front of its
+// tokens.  h0: the state at the block's start; returns in `end` (of the last lane)
+// that at its end.
+template <class S>
+struct Walk {
+  float e[S::R][S::NL], u[S::R][S::NL];
+  float before[S::NL], end[S::NL];
+  float sum, total;   // of the lane's steps, and of all up to its last token
+
+  __device__ __forceinline__ void run(const float (&delta)[S::R], const float (&ux)[S::R], const float (&a2)[S::NL],
+                                      const float (&B)[S::R][S::NL], const float (&h0)[S::NL]) {
+    float H[S::NL], P[S::NL];
+    sum = delta[0];
+#pragma unroll
+    for (int r = 1; r < S::R; ++r) sum += delta[r];
+#pragma unroll
+    for (int r = 0; r < S::R; ++r)
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) {
+        e[r][i] = __builtin_amdgcn_exp2f(delta[r] * a2[i]);
+        u[r][i] = ux[r] * B[r][i];
+      }
+#pragma unroll
+    for (int i = 0; i < S::NL; ++i) {
+      H[i] = u[0][i];
+#pragma unroll
+      for (int r = 1; r < S::R; ++r) H[i] = fmaf(e[r][i], H[i], u[r][i]);
+      P[i] = __builtin_amdgcn_exp2f(sum * a2[i]);
+    }
+    total = sum;
+    scan<1>(H, P);
+    scan<2>(H, P);
+    scan<4>(H, P);
+    scan<8>(H, P);
+#pragma unroll
+    for (int i = 0; i < S::NL; ++i) {
+      end[i] = fmaf(__builtin_amdgcn_exp2f(total * a2[i]), h0[i], H[i]);
+      before[i] = before_or(end[i], h0[i]);
+    }
+  }
+
+ private:
+  // (A lane with none before it gets P = 0, which nothing but 0 is multiplied by
+  // from there on.)
+  template <int K>
+  __device__ __forceinline__ void scan(float (&H)[S::NL], float (&P)[S::NL]) {
+    total += ssm::before<K>(total);
+#pragma unroll
+    for (int i = 0; i < S::NL; ++i) {
+      H[i] = fmaf(ssm::before<K>(H[i]), P[i], H[i]);
+      P[i] *= ssm::before<K>(P[i]);
+    }
+  }
+};
+
+// Where a workgroup works: a batch item, a group and up to DW of its channels.
+// Workgroups of neighbouring channels, which share lines of the rows, are on one
+// XCD: consecutive numbers go to the XCDs in turn.
+struct Where {
+  int64_t b;
+  int g, c0, channels;   // group, first channel, channels (a multiple of 8)
+  int64_t block;         // number of the block of channels, from 0 in every batch item
+  bool live;
+};
+template <int DW>
+__host__ __device__ __forceinline__ int64_t blocks_of(int D, int G) {
+  return (int64_t)G * ((D / G + DW - 1) / DW);
+}
+template <int DW>
+__device__ __forceinline__ Where where_of(int64_t B, int D, int G) {
+  const int per = (D / G + DW - 1) / DW;
+  const int64_t all = B * G * per, side = (all + 7) / 8;
+  const int64_t id = blockIdx.x % 8 * side + blockIdx.x / 8;
+  Where w;
+  w.live = id < all;
+  w.b = id / (G * per);
+  w.block = id % (G * per);
+  w.g = (int)(w.block / per);
+  const int at = (int)(w.block % per) * DW;
+  w.c0 = w.g * (D / G) + at;
+  w.channels = D / G - at < DW ? D / G - at : DW;
+  return w;
+}
+// Workgroups of a launch.
+template <int DW>
+int64_t grid_of(const Scan& a) {
+  return (a.B * blocks_of<DW>(a.D, a.G) + 7) / 8 * 8;
+}
+
+}  // namespace
+}  // namespace ssm

@@ -1,0 +1,315 @@
+// The selective scan forwards: prompts over blocks of tokens (ssm_scan.h), and
+// a few tokens at a time with the state in registers.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssm_scan.h"
+
+namespace ssm {
+namespace {
+
+// ---- prompts.  A workgroup stages the steps and inputs of its channels and B
+// and C of a block of tokens in LDS, each wave goes through its share of the
+// channels, and the sums over the states come back through LDS to be gated and
+// stored by the threads that loaded the same places.  The next block's loads are
+// in flight meanwhile.
+template <class S, bool BF>
+__global__ __launch_bounds__(S::NT) void scan_kernel(Scan a) {
+  __shared__ float4 delta4[S::DW * S::LD / 4], ux4[S::DW * S::LD / 4];
+  __shared__ float4 B4[S::TB * S::N / 4], C4[S::TB * S::N / 4];
+  __shared__ float4 a4[S::DW * S::N / 4], carry4[S::DW * S::N / 4];
+  float* const delta = reinterpret_cast<float*>(delta4);
+  float* const ux = reinterpret_cast<float*>(ux4);
+  float* const Bs = reinterpret_cast<float*>(B4);
+  float* const Cs = reinterpret_cast<float*>(C4);
+  float* const a2 = reinterpret_cast<float*>(a4);
+  float* const carry = reinterpret_cast<float*>(carry4);
+
+  const Where w = where_of<S::DW>(a.B, a.D, a.G);
+  if (!w.live) return;
+  const int tid = threadIdx.x, wave = tid / 64, q = tid % 64 / 16, l = tid % 16;
+  const int64_t b = w.b, n = tokens_of(a.lengths, b, a.T);
+
+  for (int i = tid; i < S::DW * S::N; i += S::NT) {
+    const int c = i / S::N, s = i % S::N;
+    const bool in = c < w.channels && s < a.N;
+    const int64_t at = (int64_t)(w.c0 + c) * a.N + s;
+    a2[i] = in ? a.A[at] * kLog2e : 0.f;
+    carry[i] = in && a.s_in ? a.s_in[b * a.D * a.N + at] : 0.f;
+  }
+
+  // The thread's 8 channels, and the tokens of its pieces.
+  const int c = tid % (S::DW / 8) * 8;
+  const bool mine = c < w.channels;
+  const auto token = [&](int i) { return (tid + i * S::NT) / (S::DW / 8); };   // of a block; past its end: none
+  float skip[8], bias[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) skip[k] = bias[k] = 0.f;
+  if (mine && a.skip) get8<false>(a.skip, w.c0 + c, skip);
+  if (mine && a.bias) get8<false>(a.bias, w.c0 + c, bias);
+
+  Raw8<BF> rx[S::TURNS], rdt[S::TURNS], rz[S::TURNS], rB[S::BTURNS], rC[S::BTURNS], now[S::TURNS];
+  const auto live = [&](int i, int64_t t0) { return mine && token(i) < S::TB && t0 + token(i) < n; };
+  const auto row = [&](const Tensor& t, int64_t at) { return b * t.b + at * t.t + w.c0 + c; };
+  const auto load = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) {
+      rx[i].clear();
+      rdt[i].clear();
+      if (live(i, t0)) {
+        rx[i].load(a.x.p, row(a.x, t0 + token(i)));
+        rdt[i].load(a.dt.p, row(a.dt, t0 + token(i)));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S::BTURNS; ++i) {
+      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      rB[i].clear();
+      rC[i].clear();
+      if (p < S::BPIECES && t0 + t < n && s < a.N) {
+        rB[i].load(a.b.p, b * a.b.b + (t0 + t) * a.b.t + w.g * a.b.h + s);
+        rC[i].load(a.c.p, b * a.c.b + (t0 + t) * a.c.t + w.g * a.c.h + s);
+      }
+    }
+  };
+
+  load(0);
+  for (int64_t t0 = 0; t0 < n; t0 += S::TB) {
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) {
+      const int t = token(i);
+      now[i] = rx[i];
+      if (t >= S::TB) continue;
+      const bool in = live(i, t0);
+      float x[8], v[8];
+      rx[i].get(x);
+      rdt[i].get(v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] += bias[k];
+        if (a.softplus) v[k] = softplus(v[k]);
+        const float d = in ? v[k] : 0.f;
+        delta[(c + k) * S::LD + S::at(t)] = d;
+        ux[(c + k) * S::LD + S::at(t)] = d * x[k];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S::BTURNS; ++i) {
+      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      if (p >= S::BPIECES) continue;
+      float x[8], y[8];
+      rB[i].get(x);
+      rC[i].get(y);
+#pragma unroll
+      for (int k = 0; k < 8; k += S::NL < 4 ? 2 : 4) {
+        if constexpr (S::NL < 4) {
+          *reinterpret_cast<float2*>(Bs + S::at(t, s + k)) = make_float2(x[k], x[k + 1]);
+          *reinterpret_cast<float2*>(Cs + S::at(t, s + k)) = make_float2(y[k], y[k + 1]);
+        } else {
+          *reinterpret_cast<float4*>(Bs + S::at(t, s + k)) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+          *reinterpret_cast<float4*>(Cs + S::at(t, s + k)) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+        }
+      }
+    }
+    __syncthreads();
+    if (a.z.p)
+#pragma unroll
+      for (int i = 0; i < S::TURNS; ++i) {
+        rz[i].clear();
+        if (live(i, t0)) rz[i].load(a.z.p, row(a.z, t0 + token(i)));
+      }
+    if (t0 + S::TB < n) load(t0 + S::TB);
+
+    float Bv[S::R][S::NL], Cv[S::R][S::NL];
+#pragma unroll
+    for (int r = 0; r < S::R; ++r) {
+      get_states<S::NL>(Bs + ((q * S::R + r) * kLanes + l) * S::NL, Bv[r]);
+      get_states<S::NL>(Cs + ((q * S::R + r) * kLanes + l) * S::NL, Cv[r]);
+    }
+    for (int d = wave; d < w.channels; d += S::NW) {
+      float dl[S::R], in[S::R], an[S::NL], h[S::NL], y[S::R];
+      get_tokens<S>(delta + d * S::LD, l, dl);
+      get_tokens<S>(ux + d * S::LD, l, in);
+      get_states<S::NL>(a2 + d * S::N + q * S::NL, an);
+      get_states<S::NL>(carry + d * S::N + q * S::NL, h);
+      Walk<S> k;
+      k.run(dl, in, an, Bv, h);
+      if (l == kLanes - 1) put_states<S::NL>(carry + d * S::N + q * S::NL, k.end);
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) h[i] = k.before[i];
+#pragma unroll
+      for (int r = 0; r < S::R; ++r) {
+        y[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          h[i] = fmaf(k.e[r][i], h[i], k.u[r][i]);
+          y[r] = fmaf(Cv[r][i], h[i], y[r]);
+        }
+      }
+      put_sums<S>(ux + d * S::LD, q, l, y);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) {
+      const int t = token(i);
+      if (t >= S::TB || !mine || t0 + t >= a.T) continue;
+      float x[8], y[8];
+      now[i].get(x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = fmaf(skip[k], x[k], ux[(c + k) * S::LD + S::at(t)]);
+      if (a.z.p) {
+        rz[i].get(x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] *= x[k] * sigmoid(x[k]);
+      }
+      if (t0 + t >= n)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = 0.f;
+      put8<BF>(const_cast<void*>(a.y.p), row(a.y, t0 + t), y);
+    }
+  }
+  // rows behind the last block's
+  if (mine) {
+    const float zero[8] = {};
+    for (int64_t t = (n + S::TB - 1) / S::TB * S::TB + token(0); t < a.T; t += S::NT / (S::DW / 8))
+      put8<BF>(const_cast<void*>(a.y.p), row(a.y, t), zero);
+  }
+  __syncthreads();
+  if (a.s_out)
+    for (int i = tid; i < S::DW * S::N; i += S::NT) {
+      const int d = i / S::N, s = i % S::N;
+      if (d < w.channels && s < a.N) a.s_out[b * a.D * a.N + (int64_t)(w.c0 + d) * a.N + s] = carry[i];
+    }
+}
+
+// ---- a few tokens.  Four adjacent states of a channel for each thread, N / 4
+// threads side by side for a channel (shared by lanes of one wave: N / 4 <= 16),
+// which have its state in registers.  Bound by the bytes of the states.
+//
+// The decay is carried in two positive parts, hi + lo = exp(delta A): rounded to
+// one it would be off the same way at every token, and a state that lives for
+// thousands of tokens by as many times 2^-25.  Both are positive, so that an infinite state
+// stays what it is.  Below exp(-0.35) a state lives for three tokens and one part does.
+__device__ __forceinline__ void decay_parts(float x, float& hi, float& lo) {
+  // expm1(x) = x (1 + x/2 (1 + x/3 (...))): to x^8 / 8! leaves 2^-26 of x at 0.35
+  float m = fmaf(x, 1.f / 40320.f, 1.f / 5040.f);
+  m = fmaf(m, x, 1.f / 720.f);
+  m = fmaf(m, x, 1.f / 120.f);
+  m = fmaf(m, x, 1.f / 24.f);
+  m = fmaf(m, x, 1.f / 6.f);
+  m = fmaf(m, x, 0.5f);
+  m = fmaf(m * x, x, x);
+  const float s = 1.f + m;
+  const float below = __uint_as_float(__float_as_uint(s) - 1);
+  const bool near = fabsf(x) < 0.35f;
+  hi = near ? below : exp_whole(x);
+  lo = near ? m - (below - 1.f) : 0.f;
+}
+
+template <bool BF>
+__device__ __forceinline__ float value(const void* p, int64_t i) {
+  if constexpr (BF)
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+  else
+    return static_cast<const float*>(p)[i];
+}
+template <bool BF>
+__device__ __forceinline__ float4 value4(const void* p, int64_t i) {
+  if constexpr (BF) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+  } else {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  }
+}
+
+constexpr int kStepThreads = 256;
+
+template <int LN, bool BF>   // lanes of a channel: the power of two from N / 4 on
+__global__ __launch_bounds__(kStepThreads) void step_kernel(Scan a, int64_t across) {
+  const int64_t id = (int64_t)blockIdx.x % across * kStepThreads + threadIdx.x;
+  const int64_t b = blockIdx.x / across;
+  const int64_t d = id / LN;
+  const int s = (int)(id % LN) * 4;
+  if (d >= a.D) return;   // all lanes of a channel together
+  const bool in = s < a.N;
+  const int64_t at = d * a.N + s, state = b * a.D * a.N + at;
+  const int g = (int)(d / (a.D / a.G));
+  const int n = (int)tokens_of(a.lengths, b, a.T);
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f), h = A;
+  if (in) A = *reinterpret_cast<const float4*>(a.A + at);
+  if (in && a.s_in) h = *reinterpret_cast<const float4*>(a.s_in + state);
+  const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
+  for (int t = 0; t < (int)a.T; ++t) {
+    float y = 0.f;
+    if (t < n) {
+      float4 B = make_float4(0.f, 0.f, 0.f, 0.f), C = B;
+      if (in) {
+        B = value4<BF>(a.b.p, b * a.b.b + t * a.b.t + g * a.b.h + s);
+        C = value4<BF>(a.c.p, b * a.c.b + t * a.c.t + g * a.c.h + s);
+      }
+      const float x = value<BF>(a.x.p, b * a.x.b + t * a.x.t + d);
+      float v = value<BF>(a.dt.p, b * a.dt.b + t * a.dt.t + d) + bias;
+      if (a.softplus) v = softplus(v);
+      const float ux = v * x;
+      float hi, lo;
+      const auto move = [&](float A, float B, float C, float& h) {
+        decay_parts(v * A, hi, lo);
+        // the small parts first: the state rounds once a token
+        h = fmaf(hi, h, lo != 0.f ? fmaf(lo, h, ux * B) : ux * B);
+        y = fmaf(C, h, y);
+      };
+      move(A.x, B.x, C.x, h.x);
+      move(A.y, B.y, C.y, h.y);
+      move(A.z, B.z, C.z, h.z);
+      move(A.w, B.w, C.w, h.w);
+      y = linattn::over_lanes<LN, false>(y);
+      y = fmaf(skip, x, y);
+      if (a.z.p) {
+        const float z = value<BF>(a.z.p, b * a.z.b + t * a.z.t + d);
+        y *= z * sigmoid(z);
+      }
+    }
+    if (s == 0) {
+      const int64_t to = b * a.y.b + t * a.y.t + d;
+      if constexpr (BF)
+        static_cast<uint16_t*>(const_cast<void*>(a.y.p))[to] = (uint16_t)linattn::pair(y, 0.f);
+      else
+        static_cast<float*>(const_cast<void*>(a.y.p))[to] = y;
+    }
+  }
+  if (in && a.s_out) *reinterpret_cast<float4*>(a.s_out + state) = h;
+}
+
+template <int LN>
+void launch_steps(const Scan& a, hipStream_t s) {
+  const int64_t across = ((int64_t)a.D * LN + kStepThreads - 1) / kStepThreads;
+  hipLaunchKernelGGL((a.bf16 ? step_kernel<LN, true> : step_kernel<LN, false>), dim3((unsigned)(across * a.B)),
+                     dim3(kStepThreads), 0, s, a, across);
+}
+
+template <class S>
+void launch(const Scan& a, hipStream_t s) {
+  hipLaunchKernelGGL((a.bf16 ? scan_kernel<S, true> : scan_kernel<S, false>), dim3((unsigned)grid_of<S::DW>(a)),
+                     dim3(S::NT), 0, s, a);
+}
+
+template <int NL, int R>
+void launch_blocks(const Scan& a, hipStream_t s) {
+  launch<Shape<NL, R, 16, 4>>(a, s);
+}
+
+}  // namespace
+
+size_t scan_workspace_bytes(const Scan&) { return 0; }
+
+hipError_t enqueue_scan(const Scan& a, void*, hipStream_t s) {
+  if (a.T <= kStepTokens)
+    (a.N <= 8 ? launch_steps<2> : a.N <= 16 ? launch_steps<4> : a.N <= 32 ? launch_steps<8> : launch_steps<16>)(a, s);
+  else
+    (a.N <= 8 ? launch_blocks<2, 8> : a.N <= 16 ? launch_blocks<4, 8> : a.N <= 32 ? launch_blocks<8, 4> : launch_blocks<16, 2>)(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

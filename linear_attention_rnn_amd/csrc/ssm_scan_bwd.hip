@@ -1,0 +1,504 @@
+// Gradients of the selective scan.  With m_t = sum_n C_t h_t + D x_t, s = silu(z)
+// (1 without z) and dm = dy s, the adjoint of the state runs from the last token
+// to the first:
+//
+//   g_t = C_t dm_t + exp(delta_{t+1} A) g_{t+1},  q_t = exp(delta_t A) g_t h_{t-1}
+//   dB_t = sum_d g delta x,   dC_t = sum_d dm h,  dz = dy m silu'(z)
+//   dx = delta sum_n g B + D dm,   ddelta = x sum_n g B + sum_n A q,   dA = sum_t delta q
+//
+// A workgroup has up to DW channels of a batch item.  It goes through the blocks
+// of tokens forwards once, which leaves the state at the start of each in the
+// workspace, then backwards: there each wave walks a channel forwards (ssm_scan.h), keeps
+// decays and states of the block in registers, and comes back with the adjoint, whose
+// decays over lanes are combined the same way.  Sums over channels stay in
+// registers while a wave goes through its channels, then the waves add theirs up
+// in order; the workgroups' sums are added up by a second kernel.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ssm_scan.h"
+
+namespace ssm {
+namespace {
+
+// The workspace.
+struct Sums {
+  float* states;   // [B, D, blocks of tokens][N as the lanes hold it]: at the start of each but the first
+  float* bc;       // [B, blocks of channels, T][2][N]: dB and dC
+  float* A;        // [B, D, N]
+  float* skip;     // [B, D]
+  float* bias;     // [B, D]
+};
+
+template <class S>
+struct Layout {
+  size_t states, bc, A, skip, bias, bytes;
+  int64_t blocks;   // of tokens
+  explicit Layout(const Scan& a) {
+    blocks = (a.T + S::TB - 1) / S::TB;
+    size_t at = 0;
+    const auto take = [&](size_t floats) {
+      const size_t from = at;
+      at += (floats + 3) / 4 * 16;
+      return from;
+    };
+    states = take((size_t)a.B * a.D * S::N * blocks);
+    bc = take((size_t)a.B * blocks_of<S::DW>(a.D, a.G) * a.T * 2 * a.N);
+    A = take((size_t)a.B * a.D * a.N);
+    skip = take((size_t)a.B * a.D);
+    bias = take((size_t)a.B * a.D);
+    bytes = at;
+  }
+  Sums in(void* ws) const {
+    char* p = static_cast<char*>(ws);
+    const auto f = [&](size_t at) { return reinterpret_cast<float*>(p + at); };
+    return {f(states), f(bc), f(A), f(skip), f(bias)};
+  }
+};
+
+template <class S, bool BF>
+__global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_t blocks) {
+  __shared__ float4 rows4[4][S::DW * S::LD / 4];
+  __shared__ float4 B4[S::TB * S::N / 4], C4[S::TB * S::N / 4];
+  __shared__ float4 a4[S::DW * S::N / 4], carry4[S::DW * S::N / 4], back4[S::DW * S::N / 4], dA4[S::DW * S::N / 4];
+  float* const delta = reinterpret_cast<float*>(rows4[0]);
+  float* const ux = reinterpret_cast<float*>(rows4[1]);   // then the sums of g B
+  float* const dm = reinterpret_cast<float*>(rows4[2]);   // then those of C h
+  float* const qa = reinterpret_cast<float*>(rows4[3]);   // the sums of A q / log 2
+  float* const Bs = reinterpret_cast<float*>(B4);
+  float* const Cs = reinterpret_cast<float*>(C4);
+  float* const a2 = reinterpret_cast<float*>(a4);
+  float* const carry = reinterpret_cast<float*>(carry4);   // the state at the start of the block
+  float* const back = reinterpret_cast<float*>(back4);     // the adjoint of that at its end
+  float* const dA = reinterpret_cast<float*>(dA4);
+
+  const Where w = where_of<S::DW>(a.B, a.D, a.G);
+  if (!w.live) return;
+  const int tid = threadIdx.x, wave = tid / 64, q = tid % 64 / 16, l = tid % 16;
+  const int64_t b = w.b, n = tokens_of(a.lengths, b, a.T);
+  const int64_t last = (n + S::TB - 1) / S::TB - 1;   // block; -1: none
+
+  for (int i = tid; i < S::DW * S::N; i += S::NT) {
+    const int c = i / S::N, s = i % S::N;
+    const bool in = c < w.channels && s < a.N;
+    const int64_t at = (int64_t)(w.c0 + c) * a.N + s;
+    a2[i] = in ? a.A[at] * kLog2e : 0.f;
+    carry[i] = in && a.s_in ? a.s_in[b * a.D * a.N + at] : 0.f;
+    back[i] = in && a.ds_out ? a.ds_out[b * a.D * a.N + at] : 0.f;
+    dA[i] = 0.f;
+  }
+  // The state at the start of block k of the workgroup's channel d.
+  const auto start = [&](int d, int64_t k) { return ws.states + ((b * a.D + w.c0 + d) * blocks + k) * S::N; };
+
+  const int c = tid % (S::DW / 8) * 8;
+  const bool mine = c < w.channels;
+  const auto token = [&](int i) { return (tid + i * S::NT) / (S::DW / 8); };
+  float bias[8], skip[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) bias[k] = skip[k] = 0.f;
+  if (mine && a.bias) get8<false>(a.bias, w.c0 + c, bias);
+  if (mine && a.skip) get8<false>(a.skip, w.c0 + c, skip);
+
+  Raw8<BF> rx[S::TURNS], rdt[S::TURNS], rdy[S::TURNS], rz[S::TURNS], rB[S::BTURNS], rC[S::BTURNS];
+  const auto live = [&](int i, int64_t t0) { return mine && token(i) < S::TB && t0 + token(i) < n; };
+  const auto row = [&](const Tensor& t, int64_t at) { return b * t.b + at * t.t + w.c0 + c; };
+  const auto load = [&](int64_t t0, bool all) {
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) {
+      rx[i].clear();
+      rdt[i].clear();
+      rdy[i].clear();
+      rz[i].clear();
+      if (!live(i, t0)) continue;
+      rx[i].load(a.x.p, row(a.x, t0 + token(i)));
+      rdt[i].load(a.dt.p, row(a.dt, t0 + token(i)));
+      if (!all) continue;
+      rdy[i].load(a.dy.p, row(a.dy, t0 + token(i)));
+      if (a.z.p) rz[i].load(a.z.p, row(a.z, t0 + token(i)));
+    }
+#pragma unroll
+    for (int i = 0; i < S::BTURNS; ++i) {
+      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      rB[i].clear();
+      rC[i].clear();
+      if (p >= S::BPIECES || t0 + t >= n || s >= a.N) continue;
+      rB[i].load(a.b.p, b * a.b.b + (t0 + t) * a.b.t + w.g * a.b.h + s);
+      if (all) rC[i].load(a.c.p, b * a.c.b + (t0 + t) * a.c.t + w.g * a.c.h + s);
+    }
+  };
+  const auto stage = [&](int64_t t0, bool all) {
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) {
+      const int t = token(i);
+      if (t >= S::TB) continue;
+      const bool in = live(i, t0);
+      float x[8], v[8];
+      rx[i].get(x);
+      rdt[i].get(v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] += bias[k];
+        if (a.softplus) v[k] = softplus(v[k]);
+        const float d = in ? v[k] : 0.f;
+        delta[(c + k) * S::LD + S::at(t)] = d;
+        ux[(c + k) * S::LD + S::at(t)] = d * x[k];
+      }
+      if (!all) continue;
+      float d[8];
+      rdy[i].get(d);
+      rz[i].get(x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dm[(c + k) * S::LD + S::at(t)] = a.z.p ? d[k] * (x[k] * sigmoid(x[k])) : d[k];
+    }
+#pragma unroll
+    for (int i = 0; i < S::BTURNS; ++i) {
+      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      if (p >= S::BPIECES) continue;
+      float x[8], y[8];
+      rB[i].get(x);
+      rC[i].get(y);
+#pragma unroll
+      for (int k = 0; k < 8; k += S::NL < 4 ? 2 : 4) {
+        if constexpr (S::NL < 4) {
+          *reinterpret_cast<float2*>(Bs + S::at(t, s + k)) = make_float2(x[k], x[k + 1]);
+          if (all) *reinterpret_cast<float2*>(Cs + S::at(t, s + k)) = make_float2(y[k], y[k + 1]);
+        } else {
+          *reinterpret_cast<float4*>(Bs + S::at(t, s + k)) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+          if (all) *reinterpret_cast<float4*>(Cs + S::at(t, s + k)) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+        }
+      }
+    }
+  };
+  // A lane's B or C, [R][NL], in the order of S::at(token, state).
+  const int mine_at = (q * S::R * kLanes + l) * S::NL;   // + r kLanes NL
+  const auto get_block = [&](const float* p, float(&x)[S::R][S::NL]) {
+#pragma unroll
+    for (int r = 0; r < S::R; ++r) get_states<S::NL>(p + mine_at + r * kLanes * S::NL, x[r]);
+  };
+
+  // ---- forwards: the states at the starts of the blocks
+  if (last > 0) load(0, false);
+  for (int64_t k = 0; k < last; ++k) {
+    stage(k * S::TB, false);
+    __syncthreads();
+    if (k + 1 < last) load((k + 1) * S::TB, false);
+    float Bv[S::R][S::NL];
+    get_block(Bs, Bv);
+    for (int d = wave; d < w.channels; d += S::NW) {
+      float dl[S::R], in[S::R], an[S::NL], h[S::NL];
+      get_tokens<S>(delta + d * S::LD, l, dl);
+      get_tokens<S>(ux + d * S::LD, l, in);
+      get_states<S::NL>(a2 + d * S::N + q * S::NL, an);
+      get_states<S::NL>(carry + d * S::N + q * S::NL, h);
+      Walk<S> f;
+      f.run(dl, in, an, Bv, h);
+      if (l == kLanes - 1) {
+        put_states<S::NL>(carry + d * S::N + q * S::NL, f.end);
+        put_states<S::NL>(start(d, k + 1) + q * S::NL, f.end);
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- backwards
+  float dskip[8] = {}, dbias[8] = {};
+  if (last >= 0) load(last * S::TB, true);
+  for (int64_t k = last; k >= 0; --k) {
+    const int64_t t0 = k * S::TB;
+    stage(t0, true);
+    Raw8<BF> nx[S::TURNS], ndt[S::TURNS], ndy[S::TURNS], nz[S::TURNS];
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) nx[i] = rx[i], ndt[i] = rdt[i], ndy[i] = rdy[i], nz[i] = rz[i];
+    __syncthreads();
+    if (k > 0) load(t0 - S::TB, true);
+    float Bv[S::R][S::NL], Cv[S::R][S::NL], dB[S::R][S::NL], dC[S::R][S::NL];
+    get_block(Bs, Bv);
+    get_block(Cs, Cv);
+#pragma unroll
+    for (int r = 0; r < S::R; ++r)
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) dB[r][i] = dC[r][i] = 0.f;
+    for (int d = wave; d < w.channels; d += S::NW) {
+      float dl[S::R], in[S::R], dv[S::R], an[S::NL], h0[S::NL], h[S::R][S::NL], y[S::R];
+      get_tokens<S>(delta + d * S::LD, l, dl);
+      get_tokens<S>(ux + d * S::LD, l, in);
+      get_tokens<S>(dm + d * S::LD, l, dv);
+      get_states<S::NL>(a2 + d * S::N + q * S::NL, an);
+      if (k == last && last > 0) {
+        get_states<S::NL>(carry + d * S::N + q * S::NL, h0);   // left by the way forwards
+      } else if (k > 0) {
+        get_states<S::NL>(start(d, k) + q * S::NL, h0);
+      } else {
+        const float* const s = a.s_in + (b * a.D + w.c0 + d) * a.N + q * S::NL;
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) h0[i] = a.s_in && q * S::NL + i < a.N ? s[i] : 0.f;
+      }
+      Walk<S> f;
+      f.run(dl, in, an, Bv, h0);
+#pragma unroll
+      for (int r = 0; r < S::R; ++r) {
+        y[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          h[r][i] = fmaf(f.e[r][i], r ? h[r - 1][i] : f.before[i], f.u[r][i]);
+          y[r] = fmaf(Cv[r][i], h[r][i], y[r]);
+          dC[r][i] = fmaf(dv[r], h[r][i], dC[r][i]);
+        }
+      }
+      // the adjoint that reaches the lane from the ones behind it
+      float g[S::NL];
+      {
+        float G[S::NL], P[S::NL], end[S::NL], total = f.sum;
+        get_states<S::NL>(back + d * S::N + q * S::NL, end);
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          G[i] = 0.f;
+#pragma unroll
+          for (int r = S::R - 1; r >= 0; --r) G[i] = f.e[r][i] * fmaf(Cv[r][i], dv[r], G[i]);
+          P[i] = __builtin_amdgcn_exp2f(f.sum * an[i]);
+        }
+        const auto join = [&](auto step) {
+          constexpr int K = decltype(step)::value;
+          total += behind<K>(total);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) {
+            G[i] = fmaf(behind<K>(G[i]), P[i], G[i]);
+            P[i] *= behind<K>(P[i]);
+          }
+        };
+        join(std::integral_constant<int, 1>());
+        join(std::integral_constant<int, 2>());
+        join(std::integral_constant<int, 4>());
+        join(std::integral_constant<int, 8>());
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          const float full = fmaf(__builtin_amdgcn_exp2f(total * an[i]), end[i], G[i]);
+          g[i] = behind_or(full, end[i]);
+          G[i] = full;
+        }
+        if (l == 0) put_states<S::NL>(back + d * S::N + q * S::NL, G);
+      }
+      put_sums<S>(dm + d * S::LD, q, l, y);
+      float gb[S::R], qs[S::R], da[S::NL];
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) da[i] = 0.f;
+#pragma unroll
+      for (int r = S::R - 1; r >= 0; --r) {
+        gb[r] = qs[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          g[i] = fmaf(Cv[r][i], dv[r], g[i]);
+          dB[r][i] = fmaf(in[r], g[i], dB[r][i]);
+          gb[r] = fmaf(g[i], Bv[r][i], gb[r]);
+          g[i] *= f.e[r][i];
+          const float p = g[i] * (r ? h[r - 1][i] : f.before[i]);
+          qs[r] = fmaf(p, an[i], qs[r]);
+          da[i] = fmaf(p, dl[r], da[i]);
+        }
+      }
+      put_sums<S>(ux + d * S::LD, q, l, gb);
+      put_sums<S>(qa + d * S::LD, q, l, qs);
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) {   // the last lane has the row's sum
+        da[i] += before<1>(da[i]);
+        da[i] += before<2>(da[i]);
+        da[i] += before<4>(da[i]);
+        da[i] += before<8>(da[i]);
+      }
+      if (l == kLanes - 1) {
+        float all[S::NL];
+        get_states<S::NL>(dA + d * S::N + q * S::NL, all);
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) all[i] += da[i];
+        put_states<S::NL>(dA + d * S::N + q * S::NL, all);
+      }
+    }
+    // the waves' dB and dC, added up in their order in the places of B and C
+#pragma unroll
+    for (int v = 0; v < S::NW; ++v) {
+      __syncthreads();
+      if (wave != v) continue;
+#pragma unroll
+      for (int r = 0; r < S::R; ++r) {
+        float* const pB = Bs + mine_at + r * kLanes * S::NL;
+        float* const pC = Cs + mine_at + r * kLanes * S::NL;
+        if (v > 0) {
+          float x[S::NL];
+          get_states<S::NL>(pB, x);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) dB[r][i] += x[i];
+          get_states<S::NL>(pC, x);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) dC[r][i] += x[i];
+        }
+        put_states<S::NL>(pB, dB[r]);
+        put_states<S::NL>(pC, dC[r]);
+      }
+    }
+    __syncthreads();
+    float* const bc = ws.bc + ((b * blocks_of<S::DW>(a.D, a.G) + w.block) * a.T + t0) * 2 * a.N;
+    for (int i = tid; i < S::TB * 2 * S::N / 2; i += S::NT) {   // two adjacent states
+      const int t = i / S::N, e = i % S::N * 2, s = e % S::N;
+      if (s < a.N && t0 + t < n)
+        *reinterpret_cast<float2*>(bc + (int64_t)t * 2 * a.N + (e < S::N ? 0 : a.N) + s) =
+            *reinterpret_cast<const float2*>((e < S::N ? Bs : Cs) + S::at(t, s));
+    }
+#pragma unroll
+    for (int i = 0; i < S::TURNS; ++i) {
+      const int t = token(i);
+      if (t >= S::TB || !mine || t0 + t >= a.T) continue;
+      const bool in = t0 + t < n;
+      float x[8], v[8], d[8], z[8], o[3][8];
+      nx[i].get(x);
+      ndt[i].get(v);
+      ndy[i].get(d);
+      nz[i].get(z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int at = (c + e) * S::LD + S::at(t);
+        const float m = fmaf(skip[e], x[e], dm[at]), gb = ux[at], del = delta[at];
+        float g = d[e];
+        if (a.z.p) {
+          const float s = sigmoid(z[e]);
+          o[2][e] = in ? d[e] * m * (s * fmaf(z[e], 1.f - s, 1.f)) : 0.f;
+          g *= z[e] * s;
+        }
+        float ddt = fmaf(x[e], gb, qa[at] * 0.69314718f);
+        if (a.softplus) ddt *= sigmoid(v[e] + bias[e]);
+        o[0][e] = in ? fmaf(del, gb, skip[e] * g) : 0.f;
+        o[1][e] = in ? ddt : 0.f;
+        if (in) {
+          dskip[e] = fmaf(g, x[e], dskip[e]);
+          dbias[e] += ddt;
+        }
+      }
+      put8<BF>(const_cast<void*>(a.dx.p), row(a.dx, t0 + t), o[0]);
+      put8<BF>(const_cast<void*>(a.ddt.p), row(a.ddt, t0 + t), o[1]);
+      if (a.z.p) put8<BF>(const_cast<void*>(a.dz.p), row(a.dz, t0 + t), o[2]);
+    }
+    __syncthreads();   // B and C have been read
+  }
+
+  // rows behind the last block's
+  if (mine) {
+    const float zero[8] = {};
+    for (int64_t t = (last + 1) * S::TB + token(0); t < a.T; t += S::NT / (S::DW / 8)) {
+      put8<BF>(const_cast<void*>(a.dx.p), row(a.dx, t), zero);
+      put8<BF>(const_cast<void*>(a.ddt.p), row(a.ddt, t), zero);
+      if (a.z.p) put8<BF>(const_cast<void*>(a.dz.p), row(a.dz, t), zero);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < S::DW * S::N; i += S::NT) {
+    const int d = i / S::N, s = i % S::N;
+    if (d >= w.channels || s >= a.N) continue;
+    const int64_t at = b * a.D * a.N + (int64_t)(w.c0 + d) * a.N + s;
+    ws.A[at] = dA[i];
+    if (a.ds_in) a.ds_in[at] = back[i];
+  }
+  // dD and dbias: the threads' sums of a channel in 64 bits
+  float* const join = reinterpret_cast<float*>(rows4);   // 8 floats of every thread
+  static_assert(8 * S::NT <= 4 * S::DW * S::LD, "the rows hold them");
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) join[tid * 8 + e] = v ? dbias[e] : dskip[e];
+    __syncthreads();
+    for (int d = tid; d < w.channels; d += S::NT) {
+      double s = 0.0;
+      for (int i = d / 8; i < S::NT; i += S::DW / 8) s += join[i * 8 + d % 8];
+      (v ? ws.bias : ws.skip)[b * a.D + w.c0 + d] = (float)s;
+    }
+  }
+}
+
+// dB and dC: the blocks' sums, in 64 bits; zero where no token counts.
+template <bool BF>
+__global__ __launch_bounds__(256) void bc_sum_kernel(Scan a, const float* bc, int per) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;   // over [B, G, T, 2, N / 2]
+  const int pairs = a.N / 2;
+  const int s = (int)(id % pairs) * 2;
+  const int c = (int)(id / pairs % 2);
+  const int64_t t = id / (2 * pairs) % a.T, bg = id / (2 * pairs) / a.T;
+  if (bg >= a.B * a.G) return;
+  const int64_t b = bg / a.G;
+  const int g = (int)(bg % a.G);
+  double x = 0.0, y = 0.0;
+  if (t < tokens_of(a.lengths, b, a.T)) {
+    const float* p = bc + (bg * per * a.T + t) * 2 * a.N + c * a.N + s;
+#pragma unroll 8
+    for (int i = 0; i < per; ++i) {
+      const float2 f = *reinterpret_cast<const float2*>(p + (int64_t)i * a.T * 2 * a.N);
+      x += f.x;
+      y += f.y;
+    }
+  }
+  const Tensor& to = c ? a.dc : a.db;
+  const int64_t at = b * to.b + t * to.t + g * to.h + s;
+  if constexpr (BF)
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(const_cast<void*>(to.p)) + at) = linattn::pair((float)x, (float)y);
+  else
+    *reinterpret_cast<float2*>(static_cast<float*>(const_cast<void*>(to.p)) + at) = make_float2((float)x, (float)y);
+}
+
+// dA, dD and dbias: the batch items' sums.
+__global__ __launch_bounds__(256) void table_sum_kernel(Scan a, Sums ws) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)a.D * a.N;
+  const float* p;
+  float* to;
+  int64_t at, step;
+  if (id < all)
+    p = ws.A, to = a.dA, at = id, step = all;
+  else if (id < all + a.D)
+    p = ws.skip, to = a.dskip, at = id - all, step = a.D;
+  else if (id < all + 2 * a.D)
+    p = ws.bias, to = a.dbias, at = id - all - a.D, step = a.D;
+  else
+    return;
+  if (!to) return;
+  double s = 0.0;
+#pragma unroll 8
+  for (int64_t b = 0; b < a.B; ++b) s += p[b * step + at];
+  to[at] = (float)s;
+}
+
+template <class S>
+hipError_t launch(const Scan& a, void* workspace, hipStream_t s) {
+  const Layout<S> lay(a);
+  const Sums ws = lay.in(workspace);
+  if (a.B) {
+    hipLaunchKernelGGL((a.bf16 ? scan_bwd_kernel<S, true> : scan_bwd_kernel<S, false>),
+                       dim3((unsigned)grid_of<S::DW>(a)), dim3(S::NT), 0, s, a, ws, lay.blocks);
+    const int64_t pairs = a.B * a.G * a.T * a.N;
+    if (pairs)
+      hipLaunchKernelGGL((a.bf16 ? bc_sum_kernel<true> : bc_sum_kernel<false>), dim3((unsigned)((pairs + 255) / 256)),
+                         dim3(256), 0, s, a, ws.bc, (int)(blocks_of<S::DW>(a.D, a.G) / a.G));
+  }
+  const int64_t all = (int64_t)a.D * (a.N + 2);
+  hipLaunchKernelGGL(table_sum_kernel, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, a, ws);
+  return hipGetLastError();
+}
+
+// Calls f with the instance that a call runs on.
+template <class F>
+auto with_shape(const Scan& a, F f) {
+  return a.N <= 8    ? f(Shape<2, 8, 32, 8>())
+         : a.N <= 16 ? f(Shape<4, 8, 32, 8>())
+         : a.N <= 32 ? f(Shape<8, 4, 32, 8>())
+                     : f(Shape<16, 2, 32, 8>());
+}
+
+}  // namespace
+
+size_t scan_bwd_workspace_bytes(const Scan& a) {
+  return with_shape(a, [&](auto s) { return Layout<decltype(s)>(a).bytes; });
+}
+
+hipError_t enqueue_scan_bwd(const Scan& a, void* workspace, hipStream_t stream) {
+  return with_shape(a, [&](auto s) { return launch<decltype(s)>(a, workspace, stream); });
+}
+
+}  // namespace ssm
