@@ -131,7 +131,7 @@ size_t ssm_conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t W, 
  *   T == 0    s_out receives s_in (or zero).  B == 0: nothing is done.
  * B * T * G * N is below 2^32.
  *
- * Calls of at most 4 tokens run token by token, longer ones over blocks of 32 to
+ * Calls of at most 8 tokens run token by token, longer ones over blocks of 32 to
  * 128 tokens whose tokens lie side by side over lanes.
  */
 int ssm_scan_fwd(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const void* x, const void* dt, const float* A,

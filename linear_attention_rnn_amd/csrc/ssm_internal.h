@@ -34,7 +34,7 @@ size_t conv_bwd_workspace_bytes(const Conv& a);
 hipError_t enqueue_conv_bwd(const Conv& a, void* workspace, hipStream_t stream);
 
 // Calls of at most so many tokens run token by token.
-constexpr int kStepTokens = 4;
+constexpr int kStepTokens = 8;
 
 struct Scan {
   int64_t B, T;

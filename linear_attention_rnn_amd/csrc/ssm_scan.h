@@ -29,28 +29,38 @@ namespace {
 
 constexpr int kLanes = 16;   // lanes over a block's tokens
 
-// Sizes of one instance: NL states a lane, R tokens a lane, DW channels and NW
-// waves a workgroup.
-template <int NL_, int R_, int DW_, int NW_>
+// Sizes of one instance: NL states and R tokens a lane, up to NG groups of 4 NL
+// states one after another, DW channels and NW waves a workgroup, PC channels that
+// a thread loads of a token.
+template <int NL_, int R_, int NG_, int DW_, int NW_, int PC_>
 struct Shape {
-  static constexpr int NL = NL_, R = R_, DW = DW_, NW = NW_;
-  static constexpr int N = 4 * NL, TB = kLanes * R, NT = 64 * NW;
+  static constexpr int NL = NL_, R = R_, NG = NG_, DW = DW_, NW = NW_, PC = PC_;
+  static constexpr int NS = 4 * NL, N = NG * NS, TB = kLanes * R, NT = 64 * NW;
   static constexpr int V = R < 4 ? R : 4;       // tokens of one access to a channel's row
   static constexpr int LD = TB + 4;             // floats of a channel's row
-  static constexpr int PIECES = TB * (DW / 8);  // of 8 channels of a token
+  static constexpr int PIECES = TB * (DW / PC);
   static constexpr int TURNS = (PIECES + NT - 1) / NT;
   static constexpr int BPIECES = TB * (N / 8);  // of 8 states of a token
   static constexpr int BTURNS = (BPIECES + NT - 1) / NT;
-  // Where token t of a block lies in a channel's row: the lanes' first V tokens
-  // side by side, then their next, so that a wave reads whole lines.
+  // Where token t of a block lies in a channel's row: the lanes' first four tokens
+  // side by side, then their next, so that a wave reads whole lines; the next are
+  // shifted by four lanes, so that adjacent tokens of a thread's neighbours meet in
+  // no bank.
   static __device__ __forceinline__ int at(int t) {
     if constexpr (R <= 4)
       return t;
     else
-      return t % R / 4 * (4 * kLanes) + t / R * 4 + t % 4;
+      return t % R / 4 * (4 * kLanes) + half(t / R, t % R) + t % 4;
   }
-  // Where B and C of token t, states from n on, lie: lanes side by side.
-  static __device__ __forceinline__ int at(int t, int n) { return ((n / NL * R + t % R) * kLanes + t / R) * NL + n % NL; }
+  static __device__ __forceinline__ int half(int l, int r) { return (l ^ (r & 4)) * 4; }
+  // Where B and C of token t, states from n on, lie: group after group, lanes side
+  // by side.
+  static __device__ __forceinline__ int at(int t, int n) { return (n / NL * R + t % R) * STEP + t / R * NL + n % NL; }
+  static constexpr int STEP = kLanes * NL;   // from one of a lane's tokens to the next
+  // Token and first state of a thread's piece of B and C: those of a wave lie side by
+  // side in LDS.
+  static __device__ __forceinline__ int piece_token(int p) { return p % kLanes * R + p / kLanes % R; }
+  static __device__ __forceinline__ int piece_state(int p) { return p / TB * 8; }
 };
 
 // A lane's tokens of a channel's row.
@@ -58,7 +68,7 @@ template <class S>
 __device__ __forceinline__ void get_tokens(const float* row, int l, float (&x)[S::R]) {
 #pragma unroll
   for (int i = 0; i < S::R; i += S::V) {
-    const float* p = row + i / 4 * (4 * kLanes) + l * S::V;
+    const float* p = row + i / 4 * (4 * kLanes) + (S::R > 4 ? S::half(l, i) : l * S::V);
     if constexpr (S::V == 4) {
       const float4 f = *reinterpret_cast<const float4*>(p);
       x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
@@ -82,6 +92,12 @@ __device__ __forceinline__ void get_states(const float* p, float (&x)[NL]) {
     }
   }
 }
+// B or C of a lane's tokens in group g.
+template <class S>
+__device__ __forceinline__ void get_block(const float* p, int g, int q, int l, float (&x)[S::R][S::NL]) {
+#pragma unroll
+  for (int r = 0; r < S::R; ++r) get_states<S::NL>(p + ((g * 4 + q) * S::R + r) * S::STEP + l * S::NL, x[r]);
+}
 template <int NL>
 __device__ __forceinline__ void put_states(float* p, const float (&x)[NL]) {
   if constexpr (NL == 2) {
@@ -93,19 +109,21 @@ __device__ __forceinline__ void put_states(float* p, const float (&x)[NL]) {
 }
 
 // Sums over the four lanes of a token's states, put into the lane's channel row
-// at its tokens.  The lane exchanges add up two tokens at a time.
+// at its tokens, or added to what earlier groups of states left there.  The lane exchanges add up two
+// tokens at a time.
 template <class S>
-__device__ __forceinline__ void put_sums(float* row, int q, int l, const float (&y)[S::R]) {
+__device__ __forceinline__ void put_sums(float* row, int q, int l, const float (&y)[S::R], bool add) {
+  const auto put = [&](float* at, float z) { *at = S::NG > 1 && add ? *at + z : z; };
   if constexpr (S::R == 2) {
     const float w = halves_sum(y[0], y[1]);
     const float z = rows16_sum(w, w);   // rows 0, 1: the first token, 2, 3: the second
-    if (q % 2 == 0) row[2 * l + q / 2] = z;
+    if (q % 2 == 0) put(row + 2 * l + q / 2, z);
   } else {
 #pragma unroll
     for (int i = 0; i < S::R; i += 4) {
       const float z = rows16_sum(halves_sum(y[i], y[i + 1]), halves_sum(y[i + 2], y[i + 3]));
       // rows 0 to 3 hold tokens 0, 2, 1, 3
-      row[i / 4 * (4 * kLanes) + 4 * l + (q % 2 * 2 + q / 2)] = z;
+      put(row + i / 4 * (4 * kLanes) + S::half(l, i) + (q % 2 * 2 + q / 2), z);
     }
   }
 }
@@ -131,14 +149,10 @@ struct Walk {
       for (int i = 0; i < S::NL; ++i) {
         e[r][i] = __builtin_amdgcn_exp2f(delta[r] * a2[i]);
         u[r][i] = ux[r] * B[r][i];
+        H[i] = r ? fmaf(e[r][i], H[i], u[r][i]) : u[r][i];
       }
 #pragma unroll
-    for (int i = 0; i < S::NL; ++i) {
-      H[i] = u[0][i];
-#pragma unroll
-      for (int r = 1; r < S::R; ++r) H[i] = fmaf(e[r][i], H[i], u[r][i]);
-      P[i] = __builtin_amdgcn_exp2f(sum * a2[i]);
-    }
+    for (int i = 0; i < S::NL; ++i) P[i] = __builtin_amdgcn_exp2f(sum * a2[i]);
     total = sum;
     scan<1>(H, P);
     scan<2>(H, P);
@@ -157,12 +171,27 @@ struct Walk {
   template <int K>
   __device__ __forceinline__ void scan(float (&H)[S::NL], float (&P)[S::NL]) {
     total += ssm::before<K>(total);
+    add_before<K>(H, P);
+    if constexpr (K < 8)
 #pragma unroll
-    for (int i = 0; i < S::NL; ++i) {
-      H[i] = fmaf(ssm::before<K>(H[i]), P[i], H[i]);
-      P[i] *= ssm::before<K>(P[i]);
-    }
+      for (int i = 0; i < S::NL; ++i) P[i] *= ssm::before<K>(P[i]);
   }
+};
+
+// x, but what is computed from it is computed where it is used: addresses of the
+// phases around the walk over the channels would keep dozens of registers through
+// it, which cost waves.
+__device__ __forceinline__ int anew(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// A thread's pieces of a block: S::PC channels from c on of the tokens token(i).
+template <class S, bool ANEW = true>
+struct Pieces {
+  int tid, c;
+  __device__ __forceinline__ explicit Pieces(int thread) : tid(ANEW ? anew(thread) : thread), c(tid % (S::DW / S::PC) * S::PC) {}
+  __device__ __forceinline__ int token(int i) const { return (tid + i * S::NT) / (S::DW / S::PC); }   // from S::TB on: none
 };
 
 // Where a workgroup works: a batch item, a group and up to DW of its channels.

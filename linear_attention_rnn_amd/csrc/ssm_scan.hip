@@ -13,13 +13,15 @@ namespace {
 // channels, and the sums over the states come back through LDS to be gated and
 // stored by the threads that loaded the same places.  The next block's loads are
 // in flight meanwhile.
-template <class S, bool BF>
-__global__ __launch_bounds__(S::NT) void scan_kernel(Scan a) {
-  __shared__ float4 delta4[S::DW * S::LD / 4], ux4[S::DW * S::LD / 4];
+template <class S, bool AHEAD, bool BF>
+__global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
+  __shared__ float4 delta4[S::DW * S::LD / 4], ux4[S::DW * S::LD / 4], y4[S::NG > 1 ? S::DW * S::LD / 4 : 1];
   __shared__ float4 B4[S::TB * S::N / 4], C4[S::TB * S::N / 4];
   __shared__ float4 a4[S::DW * S::N / 4], carry4[S::DW * S::N / 4];
+  __shared__ float tables[2][S::DW];
   float* const delta = reinterpret_cast<float*>(delta4);
   float* const ux = reinterpret_cast<float*>(ux4);
+  float* const ys = S::NG > 1 ? reinterpret_cast<float*>(y4) : ux;   // the sums of C h
   float* const Bs = reinterpret_cast<float*>(B4);
   float* const Cs = reinterpret_cast<float*>(C4);
   float* const a2 = reinterpret_cast<float*>(a4);
@@ -38,32 +40,33 @@ __global__ __launch_bounds__(S::NT) void scan_kernel(Scan a) {
     carry[i] = in && a.s_in ? a.s_in[b * a.D * a.N + at] : 0.f;
   }
 
-  // The thread's 8 channels, and the tokens of its pieces.
-  const int c = tid % (S::DW / 8) * 8;
-  const bool mine = c < w.channels;
-  const auto token = [&](int i) { return (tid + i * S::NT) / (S::DW / 8); };   // of a block; past its end: none
-  float skip[8], bias[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) skip[k] = bias[k] = 0.f;
-  if (mine && a.skip) get8<false>(a.skip, w.c0 + c, skip);
-  if (mine && a.bias) get8<false>(a.bias, w.c0 + c, bias);
+  for (int i = tid; i < 2 * S::DW; i += S::NT) {
+    const float* const from = i < S::DW ? a.skip : a.bias;
+    tables[i / S::DW][i % S::DW] = from && i % S::DW < w.channels ? from[w.c0 + i % S::DW] : 0.f;
+  }
+  using Mine = Pieces<S, !AHEAD>;
+  const auto live = [&](const Mine& me, int i, int64_t t0) {
+    return me.c < w.channels && me.token(i) < S::TB && t0 + me.token(i) < n;
+  };
+  const auto row = [&](const Mine& me, const Tensor& t, int64_t at) { return b * t.b + at * t.t + w.c0 + me.c; };
+  __syncthreads();   // the tables
 
-  Raw8<BF> rx[S::TURNS], rdt[S::TURNS], rz[S::TURNS], rB[S::BTURNS], rC[S::BTURNS], now[S::TURNS];
-  const auto live = [&](int i, int64_t t0) { return mine && token(i) < S::TB && t0 + token(i) < n; };
-  const auto row = [&](const Tensor& t, int64_t at) { return b * t.b + at * t.t + w.c0 + c; };
+  Raw<BF, S::PC> rx[S::TURNS], rdt[S::TURNS], now[S::TURNS], rz[S::TURNS];
+  Raw8<BF> rB[S::BTURNS], rC[S::BTURNS];
   const auto load = [&](int64_t t0) {
+    const Mine me(tid);
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
       rx[i].clear();
       rdt[i].clear();
-      if (live(i, t0)) {
-        rx[i].load(a.x.p, row(a.x, t0 + token(i)));
-        rdt[i].load(a.dt.p, row(a.dt, t0 + token(i)));
+      if (live(me, i, t0)) {
+        rx[i].load(a.x.p, row(me, a.x, t0 + me.token(i)));
+        rdt[i].load(a.dt.p, row(me, a.dt, t0 + me.token(i)));
       }
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
       rB[i].clear();
       rC[i].clear();
       if (p < S::BPIECES && t0 + t < n && s < a.N) {
@@ -72,22 +75,34 @@ __global__ __launch_bounds__(S::NT) void scan_kernel(Scan a) {
       }
     }
   };
+  // The inputs of the output's factor and skip.
+  const auto load_out = [&](const Mine& me, int64_t t0, int i) {
+    if (!live(me, i, t0)) return;
+    now[i].load(a.x.p, row(me, a.x, t0 + me.token(i)));
+    if (a.z.p) rz[i].load(a.z.p, row(me, a.z, t0 + me.token(i)));
+  };
 
-  load(0);
+  if (AHEAD && n) load(0);
   for (int64_t t0 = 0; t0 < n; t0 += S::TB) {
+    if (!AHEAD) load(t0);
+    const Mine me(tid);
+    const int c = me.c;
+    const float* const bias = tables[1] + c;
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
-      const int t = token(i);
-      now[i] = rx[i];
+      const int t = me.token(i);
       if (t >= S::TB) continue;
-      const bool in = live(i, t0);
-      float x[8], v[8];
+      const bool in = live(me, i, t0);
+      float x[S::PC], v[S::PC];
       rx[i].get(x);
       rdt[i].get(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] += bias[k];
-        if (a.softplus) v[k] = softplus(v[k]);
+      for (int k = 0; k < S::PC; ++k) v[k] += bias[k];
+      if (a.softplus)   // (one branch around all of them: their chains overlap)
+#pragma unroll
+        for (int k = 0; k < S::PC; ++k) v[k] = softplus(v[k]);
+#pragma unroll
+      for (int k = 0; k < S::PC; ++k) {
         const float d = in ? v[k] : 0.f;
         delta[(c + k) * S::LD + S::at(t)] = d;
         ux[(c + k) * S::LD + S::at(t)] = d * x[k];
@@ -95,7 +110,7 @@ __global__ __launch_bounds__(S::NT) void scan_kernel(Scan a) {
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
       if (p >= S::BPIECES) continue;
       float x[8], y[8];
       rB[i].get(x);
@@ -112,67 +127,72 @@ __global__ __launch_bounds__(S::NT) void scan_kernel(Scan a) {
       }
     }
     __syncthreads();
-    if (a.z.p)
+    if (AHEAD) {
 #pragma unroll
-      for (int i = 0; i < S::TURNS; ++i) {
-        rz[i].clear();
-        if (live(i, t0)) rz[i].load(a.z.p, row(a.z, t0 + token(i)));
-      }
-    if (t0 + S::TB < n) load(t0 + S::TB);
-
-    float Bv[S::R][S::NL], Cv[S::R][S::NL];
-#pragma unroll
-    for (int r = 0; r < S::R; ++r) {
-      get_states<S::NL>(Bs + ((q * S::R + r) * kLanes + l) * S::NL, Bv[r]);
-      get_states<S::NL>(Cs + ((q * S::R + r) * kLanes + l) * S::NL, Cv[r]);
+      for (int i = 0; i < S::TURNS; ++i) load_out(me, t0, i);
+      if (t0 + S::TB < n) load(t0 + S::TB);
     }
-    for (int d = wave; d < w.channels; d += S::NW) {
-      float dl[S::R], in[S::R], an[S::NL], h[S::NL], y[S::R];
-      get_tokens<S>(delta + d * S::LD, l, dl);
-      get_tokens<S>(ux + d * S::LD, l, in);
-      get_states<S::NL>(a2 + d * S::N + q * S::NL, an);
-      get_states<S::NL>(carry + d * S::N + q * S::NL, h);
-      Walk<S> k;
-      k.run(dl, in, an, Bv, h);
-      if (l == kLanes - 1) put_states<S::NL>(carry + d * S::N + q * S::NL, k.end);
+#pragma unroll 1
+    for (int g = 0; g * S::NS < a.N; ++g) {
+#pragma unroll 1
+      for (int d = wave; d < w.channels; d += S::NW) {
+        const int states = d * S::N + g * S::NS + q * S::NL;
+        float dl[S::R], in[S::R], an[S::NL], h[S::NL], y[S::R], v[S::R][S::NL];
+        get_tokens<S>(delta + d * S::LD, l, dl);
+        get_tokens<S>(ux + d * S::LD, l, in);
+        get_states<S::NL>(a2 + states, an);
+        get_states<S::NL>(carry + states, h);
+        asm volatile("" ::: "memory");   // B and C are read for every channel: registers for them would halve the waves
+        get_block<S>(Bs, g, q, l, v);
+        Walk<S> k;
+        k.run(dl, in, an, v, h);
+        if (l == kLanes - 1) put_states<S::NL>(carry + states, k.end);
+        asm volatile("" ::: "memory");
+        get_block<S>(Cs, g, q, l, v);
 #pragma unroll
-      for (int i = 0; i < S::NL; ++i) h[i] = k.before[i];
+        for (int r = 0; r < S::R; ++r) {
+          y[r] = 0.f;
 #pragma unroll
-      for (int r = 0; r < S::R; ++r) {
-        y[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < S::NL; ++i) {
-          h[i] = fmaf(k.e[r][i], h[i], k.u[r][i]);
-          y[r] = fmaf(Cv[r][i], h[i], y[r]);
+          for (int i = 0; i < S::NL; ++i) {
+            k.before[i] = fmaf(k.e[r][i], k.before[i], k.u[r][i]);
+            y[r] = fmaf(v[r][i], k.before[i], y[r]);
+          }
         }
+        put_sums<S>(ys + d * S::LD, q, l, y, g > 0);
       }
-      put_sums<S>(ux + d * S::LD, q, l, y);
     }
     __syncthreads();
+    const Mine out(tid);
+    const float* const skip = tables[0] + out.c;
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
-      const int t = token(i);
-      if (t >= S::TB || !mine || t0 + t >= a.T) continue;
-      float x[8], y[8];
-      now[i].get(x);
+      const int t = out.token(i);
+      if (t >= S::TB || out.c >= w.channels || t0 + t >= a.T) continue;
+      const bool in = t0 + t < n;
+      Raw<BF, S::PC> r;
+      r.clear();
+      if (in) {
+        float x[S::PC], y[S::PC];
+        if (!AHEAD) load_out(out, t0, i);
+        now[i].get(x);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = fmaf(skip[k], x[k], ux[(c + k) * S::LD + S::at(t)]);
-      if (a.z.p) {
-        rz[i].get(x);
+        for (int k = 0; k < S::PC; ++k) y[k] = fmaf(skip[k], x[k], ys[(out.c + k) * S::LD + S::at(t)]);
+        if (a.z.p) {
+          rz[i].get(x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= x[k] * sigmoid(x[k]);
+          for (int k = 0; k < S::PC; ++k) y[k] *= x[k] * sigmoid<BF>(x[k]);
+        }
+        r.set(y);
       }
-      if (t0 + t >= n)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = 0.f;
-      put8<BF>(const_cast<void*>(a.y.p), row(a.y, t0 + t), y);
+      r.store(const_cast<void*>(a.y.p), row(out, a.y, t0 + t));
     }
   }
   // rows behind the last block's
-  if (mine) {
-    const float zero[8] = {};
-    for (int64_t t = (n + S::TB - 1) / S::TB * S::TB + token(0); t < a.T; t += S::NT / (S::DW / 8))
-      put8<BF>(const_cast<void*>(a.y.p), row(a.y, t), zero);
+  if (const Mine me(tid); me.c < w.channels) {
+    Raw<BF, S::PC> zero;
+    zero.clear();
+    for (int64_t t = (n + S::TB - 1) / S::TB * S::TB + me.token(0); t < a.T; t += S::NT / (S::DW / S::PC))
+      zero.store(const_cast<void*>(a.y.p), row(me, a.y, t));
   }
   __syncthreads();
   if (a.s_out)
@@ -289,15 +309,27 @@ void launch_steps(const Scan& a, hipStream_t s) {
                      dim3(kStepThreads), 0, s, a, across);
 }
 
-template <class S>
+template <class S, bool AHEAD>
 void launch(const Scan& a, hipStream_t s) {
-  hipLaunchKernelGGL((a.bf16 ? scan_kernel<S, true> : scan_kernel<S, false>), dim3((unsigned)grid_of<S::DW>(a)),
+  hipLaunchKernelGGL((a.bf16 ? scan_kernel<S, AHEAD, true> : scan_kernel<S, AHEAD, false>), dim3((unsigned)grid_of<S::DW>(a)),
                      dim3(S::NT), 0, s, a);
 }
 
-template <int NL, int R>
+template <int NL, int R, int NG>
 void launch_blocks(const Scan& a, hipStream_t s) {
-  launch<Shape<NL, R, 16, 4>>(a, s);
+  const int64_t groups = a.B * blocks_of<8>(a.D, a.G);   // of 8 channels
+  if (NG == 4 ? groups < 1024 : groups < 400)
+    launch<Shape<NL, R, NG, 8, 8, 4>, true>(a, s);
+  else if constexpr (NG == 4)
+    launch<Shape<NL, R, NG, 32, 8, 8>, false>(a, s);
+  else if (NG == 2 || groups < 1024)
+    launch<Shape<NL, R, NG, 8, 4, 4>, false>(a, s);
+  else
+    launch<Shape<NL, R, NG, 16, 4, 8>, false>(a, s);
+}
+template <int R>
+void launch_tokens(const Scan& a, hipStream_t s) {
+  (a.N <= 8 ? launch_blocks<2, R, 1> : a.N <= 16 ? launch_blocks<4, R, 1> : a.N <= 32 ? launch_blocks<4, R, 2> : launch_blocks<4, R, 4>)(a, s);
 }
 
 }  // namespace
@@ -308,7 +340,7 @@ hipError_t enqueue_scan(const Scan& a, void*, hipStream_t s) {
   if (a.T <= kStepTokens)
     (a.N <= 8 ? launch_steps<2> : a.N <= 16 ? launch_steps<4> : a.N <= 32 ? launch_steps<8> : launch_steps<16>)(a, s);
   else
-    (a.N <= 8 ? launch_blocks<2, 8> : a.N <= 16 ? launch_blocks<4, 8> : a.N <= 32 ? launch_blocks<8, 4> : launch_blocks<16, 2>)(a, s);
+    (a.T <= 32 ? launch_tokens<2> : a.T <= 64 ? launch_tokens<4> : launch_tokens<8>)(a, s);
   return hipGetLastError();
 }
 

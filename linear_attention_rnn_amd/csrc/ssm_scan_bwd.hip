@@ -60,13 +60,18 @@ struct Layout {
 
 template <class S, bool BF>
 __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_t blocks) {
-  __shared__ float4 rows4[4][S::DW * S::LD / 4];
+  // With several groups of states the inputs of the next are not overwritten.
+  constexpr int ROWS = S::NG > 1 ? 6 : 4;
+  __shared__ float4 rows4[ROWS][S::DW * S::LD / 4];
   __shared__ float4 B4[S::TB * S::N / 4], C4[S::TB * S::N / 4];
   __shared__ float4 a4[S::DW * S::N / 4], carry4[S::DW * S::N / 4], back4[S::DW * S::N / 4], dA4[S::DW * S::N / 4];
+  __shared__ float tables[2][S::DW];
   float* const delta = reinterpret_cast<float*>(rows4[0]);
-  float* const ux = reinterpret_cast<float*>(rows4[1]);   // then the sums of g B
-  float* const dm = reinterpret_cast<float*>(rows4[2]);   // then those of C h
-  float* const qa = reinterpret_cast<float*>(rows4[3]);   // the sums of A q / log 2
+  float* const ux = reinterpret_cast<float*>(rows4[1]);
+  float* const dm = reinterpret_cast<float*>(rows4[2]);
+  float* const qa = reinterpret_cast<float*>(rows4[3]);                            // the sums of A q / log 2,
+  float* const gbs = reinterpret_cast<float*>(rows4[S::NG > 1 ? ROWS - 2 : 1]);    // of g B
+  float* const ys = reinterpret_cast<float*>(rows4[S::NG > 1 ? ROWS - 1 : 2]);     // and of C h
   float* const Bs = reinterpret_cast<float*>(B4);
   float* const Cs = reinterpret_cast<float*>(C4);
   float* const a2 = reinterpret_cast<float*>(a4);
@@ -89,72 +94,82 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
     back[i] = in && a.ds_out ? a.ds_out[b * a.D * a.N + at] : 0.f;
     dA[i] = 0.f;
   }
+  for (int i = tid; i < 2 * S::DW; i += S::NT) {
+    const float* const from = i < S::DW ? a.skip : a.bias;
+    tables[i / S::DW][i % S::DW] = from && i % S::DW < w.channels ? from[w.c0 + i % S::DW] : 0.f;
+  }
   // The state at the start of block k of the workgroup's channel d.
   const auto start = [&](int d, int64_t k) { return ws.states + ((b * a.D + w.c0 + d) * blocks + k) * S::N; };
 
-  const int c = tid % (S::DW / 8) * 8;
-  const bool mine = c < w.channels;
-  const auto token = [&](int i) { return (tid + i * S::NT) / (S::DW / 8); };
-  float bias[8], skip[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) bias[k] = skip[k] = 0.f;
-  if (mine && a.bias) get8<false>(a.bias, w.c0 + c, bias);
-  if (mine && a.skip) get8<false>(a.skip, w.c0 + c, skip);
+  const auto live = [&](const Pieces<S>& me, int i, int64_t t0) {
+    return me.c < w.channels && me.token(i) < S::TB && t0 + me.token(i) < n;
+  };
+  const auto row = [&](const Pieces<S>& me, const Tensor& t, int64_t at) { return b * t.b + at * t.t + w.c0 + me.c; };
+  using Piece = Raw<BF, S::PC>;
 
-  Raw8<BF> rx[S::TURNS], rdt[S::TURNS], rdy[S::TURNS], rz[S::TURNS], rB[S::BTURNS], rC[S::BTURNS];
-  const auto live = [&](int i, int64_t t0) { return mine && token(i) < S::TB && t0 + token(i) < n; };
-  const auto row = [&](const Tensor& t, int64_t at) { return b * t.b + at * t.t + w.c0 + c; };
-  const auto load = [&](int64_t t0, bool all) {
+  // A block's steps and inputs, and with ALL its C and gradients of y.
+  const auto stage = [&](int64_t t0, auto ALL) {
+    constexpr bool all = decltype(ALL)::value;
+    const Pieces<S> me(tid);
+    const int c = me.c;
+    const float* const bias = tables[1] + c;
+    Piece rx[S::TURNS], rdt[S::TURNS], rdy[S::TURNS], rz[S::TURNS];
+    Raw8<BF> rB[S::BTURNS], rC[S::BTURNS];
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
       rx[i].clear();
       rdt[i].clear();
       rdy[i].clear();
       rz[i].clear();
-      if (!live(i, t0)) continue;
-      rx[i].load(a.x.p, row(a.x, t0 + token(i)));
-      rdt[i].load(a.dt.p, row(a.dt, t0 + token(i)));
-      if (!all) continue;
-      rdy[i].load(a.dy.p, row(a.dy, t0 + token(i)));
-      if (a.z.p) rz[i].load(a.z.p, row(a.z, t0 + token(i)));
+      if (!live(me, i, t0)) continue;
+      rx[i].load(a.x.p, row(me, a.x, t0 + me.token(i)));
+      rdt[i].load(a.dt.p, row(me, a.dt, t0 + me.token(i)));
+      if constexpr (all) {
+        rdy[i].load(a.dy.p, row(me, a.dy, t0 + me.token(i)));
+        if (a.z.p) rz[i].load(a.z.p, row(me, a.z, t0 + me.token(i)));
+      }
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
       rB[i].clear();
       rC[i].clear();
       if (p >= S::BPIECES || t0 + t >= n || s >= a.N) continue;
       rB[i].load(a.b.p, b * a.b.b + (t0 + t) * a.b.t + w.g * a.b.h + s);
-      if (all) rC[i].load(a.c.p, b * a.c.b + (t0 + t) * a.c.t + w.g * a.c.h + s);
+      if constexpr (all) rC[i].load(a.c.p, b * a.c.b + (t0 + t) * a.c.t + w.g * a.c.h + s);
     }
-  };
-  const auto stage = [&](int64_t t0, bool all) {
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
-      const int t = token(i);
+      const int t = me.token(i);
       if (t >= S::TB) continue;
-      const bool in = live(i, t0);
-      float x[8], v[8];
+      const bool in = live(me, i, t0);
+      float x[S::PC], v[S::PC];
       rx[i].get(x);
       rdt[i].get(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] += bias[k];
-        if (a.softplus) v[k] = softplus(v[k]);
+      for (int k = 0; k < S::PC; ++k) v[k] += bias[k];
+      if (a.softplus)   // (one branch around all of them: their chains overlap)
+#pragma unroll
+        for (int k = 0; k < S::PC; ++k) v[k] = softplus(v[k]);
+#pragma unroll
+      for (int k = 0; k < S::PC; ++k) {
         const float d = in ? v[k] : 0.f;
         delta[(c + k) * S::LD + S::at(t)] = d;
         ux[(c + k) * S::LD + S::at(t)] = d * x[k];
       }
-      if (!all) continue;
-      float d[8];
-      rdy[i].get(d);
-      rz[i].get(x);
+      if constexpr (all) {
+        rdy[i].get(v);
+        rz[i].get(x);
+        if (a.z.p)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dm[(c + k) * S::LD + S::at(t)] = a.z.p ? d[k] * (x[k] * sigmoid(x[k])) : d[k];
+          for (int k = 0; k < S::PC; ++k) v[k] *= x[k] * sigmoid(x[k]);
+#pragma unroll
+        for (int k = 0; k < S::PC; ++k) dm[(c + k) * S::LD + S::at(t)] = v[k];
+      }
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = tid + i * S::NT, t = p / (S::N / 8), s = p % (S::N / 8) * 8;
+      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
       if (p >= S::BPIECES) continue;
       float x[8], y[8];
       rB[i].get(x);
@@ -171,102 +186,102 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
       }
     }
   };
-  // A lane's B or C, [R][NL], in the order of S::at(token, state).
-  const int mine_at = (q * S::R * kLanes + l) * S::NL;   // + r kLanes NL
-  const auto get_block = [&](const float* p, float(&x)[S::R][S::NL]) {
-#pragma unroll
-    for (int r = 0; r < S::R; ++r) get_states<S::NL>(p + mine_at + r * kLanes * S::NL, x[r]);
-  };
 
   // ---- forwards: the states at the starts of the blocks
-  if (last > 0) load(0, false);
   for (int64_t k = 0; k < last; ++k) {
-    stage(k * S::TB, false);
     __syncthreads();
-    if (k + 1 < last) load((k + 1) * S::TB, false);
-    float Bv[S::R][S::NL];
-    get_block(Bs, Bv);
-    for (int d = wave; d < w.channels; d += S::NW) {
-      float dl[S::R], in[S::R], an[S::NL], h[S::NL];
-      get_tokens<S>(delta + d * S::LD, l, dl);
-      get_tokens<S>(ux + d * S::LD, l, in);
-      get_states<S::NL>(a2 + d * S::N + q * S::NL, an);
-      get_states<S::NL>(carry + d * S::N + q * S::NL, h);
-      Walk<S> f;
-      f.run(dl, in, an, Bv, h);
-      if (l == kLanes - 1) {
-        put_states<S::NL>(carry + d * S::N + q * S::NL, f.end);
-        put_states<S::NL>(start(d, k + 1) + q * S::NL, f.end);
+    stage(k * S::TB, std::false_type());
+    __syncthreads();
+#pragma unroll 1
+    for (int g = 0; g * S::NS < a.N; ++g) {
+#pragma unroll 1
+      for (int d = wave; d < w.channels; d += S::NW) {
+        const int states = d * S::N + g * S::NS + q * S::NL;
+        float dl[S::R], in[S::R], an[S::NL], h[S::NL], Bv[S::R][S::NL];
+        get_tokens<S>(delta + d * S::LD, l, dl);
+        get_tokens<S>(ux + d * S::LD, l, in);
+        get_states<S::NL>(a2 + states, an);
+        get_states<S::NL>(carry + states, h);
+        asm volatile("" ::: "memory");   // B is read for every channel: registers for it would cost waves
+        get_block<S>(Bs, g, q, l, Bv);
+        Walk<S> f;
+        f.run(dl, in, an, Bv, h);
+        if (l == kLanes - 1) {
+          put_states<S::NL>(carry + states, f.end);
+          put_states<S::NL>(start(d, k + 1) + g * S::NS + q * S::NL, f.end);
+        }
       }
     }
-    __syncthreads();
   }
 
   // ---- backwards
-  float dskip[8] = {}, dbias[8] = {};
-  if (last >= 0) load(last * S::TB, true);
+  float dskip[S::PC] = {}, dbias[S::PC] = {};
   for (int64_t k = last; k >= 0; --k) {
     const int64_t t0 = k * S::TB;
-    stage(t0, true);
-    Raw8<BF> nx[S::TURNS], ndt[S::TURNS], ndy[S::TURNS], nz[S::TURNS];
-#pragma unroll
-    for (int i = 0; i < S::TURNS; ++i) nx[i] = rx[i], ndt[i] = rdt[i], ndy[i] = rdy[i], nz[i] = rz[i];
     __syncthreads();
-    if (k > 0) load(t0 - S::TB, true);
-    float Bv[S::R][S::NL], Cv[S::R][S::NL], dB[S::R][S::NL], dC[S::R][S::NL];
-    get_block(Bs, Bv);
-    get_block(Cs, Cv);
+    stage(t0, std::true_type());
+    __syncthreads();
+#pragma unroll 1
+    for (int g = 0; g * S::NS < a.N; ++g) {
+      float dB[S::R][S::NL], dC[S::R][S::NL];
 #pragma unroll
-    for (int r = 0; r < S::R; ++r)
+      for (int r = 0; r < S::R; ++r)
 #pragma unroll
-      for (int i = 0; i < S::NL; ++i) dB[r][i] = dC[r][i] = 0.f;
-    for (int d = wave; d < w.channels; d += S::NW) {
-      float dl[S::R], in[S::R], dv[S::R], an[S::NL], h0[S::NL], h[S::R][S::NL], y[S::R];
-      get_tokens<S>(delta + d * S::LD, l, dl);
-      get_tokens<S>(ux + d * S::LD, l, in);
-      get_tokens<S>(dm + d * S::LD, l, dv);
-      get_states<S::NL>(a2 + d * S::N + q * S::NL, an);
-      if (k == last && last > 0) {
-        get_states<S::NL>(carry + d * S::N + q * S::NL, h0);   // left by the way forwards
-      } else if (k > 0) {
-        get_states<S::NL>(start(d, k) + q * S::NL, h0);
-      } else {
-        const float* const s = a.s_in + (b * a.D + w.c0 + d) * a.N + q * S::NL;
+        for (int i = 0; i < S::NL; ++i) dB[r][i] = dC[r][i] = 0.f;
+#pragma unroll 1
+      for (int d = wave; d < w.channels; d += S::NW) {
+        const int states = d * S::N + g * S::NS + q * S::NL;
+        float dl[S::R], in[S::R], dv[S::R], an[S::NL], h0[S::NL], h[S::R][S::NL], v[S::R][S::NL], y[S::R];
+        get_tokens<S>(delta + d * S::LD, l, dl);
+        get_tokens<S>(ux + d * S::LD, l, in);
+        get_tokens<S>(dm + d * S::LD, l, dv);
+        get_states<S::NL>(a2 + states, an);
+        if (k == last && last > 0) {
+          get_states<S::NL>(carry + states, h0);   // left by the way forwards
+        } else if (k > 0) {
+          get_states<S::NL>(start(d, k) + g * S::NS + q * S::NL, h0);
+        } else {
+          const int at = g * S::NS + q * S::NL;
+          const float* const s = a.s_in + (b * a.D + w.c0 + d) * a.N + at;
 #pragma unroll
-        for (int i = 0; i < S::NL; ++i) h0[i] = a.s_in && q * S::NL + i < a.N ? s[i] : 0.f;
-      }
-      Walk<S> f;
-      f.run(dl, in, an, Bv, h0);
-#pragma unroll
-      for (int r = 0; r < S::R; ++r) {
-        y[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < S::NL; ++i) {
-          h[r][i] = fmaf(f.e[r][i], r ? h[r - 1][i] : f.before[i], f.u[r][i]);
-          y[r] = fmaf(Cv[r][i], h[r][i], y[r]);
-          dC[r][i] = fmaf(dv[r], h[r][i], dC[r][i]);
+          for (int i = 0; i < S::NL; ++i) h0[i] = a.s_in && at + i < a.N ? s[i] : 0.f;
         }
-      }
-      // the adjoint that reaches the lane from the ones behind it
-      float g[S::NL];
-      {
-        float G[S::NL], P[S::NL], end[S::NL], total = f.sum;
-        get_states<S::NL>(back + d * S::N + q * S::NL, end);
+        asm volatile("" ::: "memory");
+        get_block<S>(Bs, g, q, l, v);
+        Walk<S> f;
+        f.run(dl, in, an, v, h0);
+        asm volatile("" ::: "memory");
+        get_block<S>(Cs, g, q, l, v);
+#pragma unroll
+        for (int r = 0; r < S::R; ++r) {
+          y[r] = 0.f;
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) {
+            h[r][i] = fmaf(f.e[r][i], r ? h[r - 1][i] : f.before[i], f.u[r][i]);
+            y[r] = fmaf(v[r][i], h[r][i], y[r]);
+            dC[r][i] = fmaf(dv[r], h[r][i], dC[r][i]);
+          }
+        }
+        // the adjoint that reaches the lane from the ones behind it
+        float G[S::NL], P[S::NL], end[S::NL], gr[S::NL], total = f.sum;
+        get_states<S::NL>(back + states, end);
 #pragma unroll
         for (int i = 0; i < S::NL; ++i) {
           G[i] = 0.f;
 #pragma unroll
-          for (int r = S::R - 1; r >= 0; --r) G[i] = f.e[r][i] * fmaf(Cv[r][i], dv[r], G[i]);
+          for (int r = S::R - 1; r >= 0; --r) {
+            v[r][i] *= dv[r];   // C dm from here on
+            G[i] = f.e[r][i] * (v[r][i] + G[i]);
+          }
           P[i] = __builtin_amdgcn_exp2f(f.sum * an[i]);
         }
         const auto join = [&](auto step) {
           constexpr int K = decltype(step)::value;
           total += behind<K>(total);
+          add_before<-K>(G, P);
+          if constexpr (K < 8)
 #pragma unroll
-          for (int i = 0; i < S::NL; ++i) {
-            G[i] = fmaf(behind<K>(G[i]), P[i], G[i]);
-            P[i] *= behind<K>(P[i]);
-          }
+            for (int i = 0; i < S::NL; ++i) P[i] *= behind<K>(P[i]);
         };
         join(std::integral_constant<int, 1>());
         join(std::integral_constant<int, 2>());
@@ -274,72 +289,78 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
         join(std::integral_constant<int, 8>());
 #pragma unroll
         for (int i = 0; i < S::NL; ++i) {
-          const float full = fmaf(__builtin_amdgcn_exp2f(total * an[i]), end[i], G[i]);
-          g[i] = behind_or(full, end[i]);
-          G[i] = full;
+          G[i] = fmaf(__builtin_amdgcn_exp2f(total * an[i]), end[i], G[i]);
+          gr[i] = behind_or(G[i], end[i]);
         }
-        if (l == 0) put_states<S::NL>(back + d * S::N + q * S::NL, G);
-      }
-      put_sums<S>(dm + d * S::LD, q, l, y);
-      float gb[S::R], qs[S::R], da[S::NL];
+        if (l == 0) put_states<S::NL>(back + states, G);
+        put_sums<S>(ys + d * S::LD, q, l, y, g > 0);
+        // back over the lane's tokens
+        float gb[S::R], qs[S::R], da[S::NL];
 #pragma unroll
-      for (int i = 0; i < S::NL; ++i) da[i] = 0.f;
+        for (int i = 0; i < S::NL; ++i) da[i] = 0.f;
+        asm volatile("" ::: "memory");
 #pragma unroll
-      for (int r = S::R - 1; r >= 0; --r) {
-        gb[r] = qs[r] = 0.f;
+        for (int r = S::R - 1; r >= 0; --r) {
+          float Br[S::NL];
+          get_states<S::NL>(Bs + ((g * 4 + q) * S::R + r) * S::STEP + l * S::NL, Br);
+          gb[r] = qs[r] = 0.f;
 #pragma unroll
-        for (int i = 0; i < S::NL; ++i) {
-          g[i] = fmaf(Cv[r][i], dv[r], g[i]);
-          dB[r][i] = fmaf(in[r], g[i], dB[r][i]);
-          gb[r] = fmaf(g[i], Bv[r][i], gb[r]);
-          g[i] *= f.e[r][i];
-          const float p = g[i] * (r ? h[r - 1][i] : f.before[i]);
-          qs[r] = fmaf(p, an[i], qs[r]);
-          da[i] = fmaf(p, dl[r], da[i]);
+          for (int i = 0; i < S::NL; ++i) {
+            gr[i] += v[r][i];
+            dB[r][i] = fmaf(in[r], gr[i], dB[r][i]);
+            gb[r] = fmaf(gr[i], Br[i], gb[r]);
+            gr[i] *= f.e[r][i];
+            const float p = gr[i] * (r ? h[r - 1][i] : f.before[i]);
+            qs[r] = fmaf(p, an[i], qs[r]);
+            da[i] = fmaf(p, dl[r], da[i]);
+          }
+        }
+        put_sums<S>(gbs + d * S::LD, q, l, gb, g > 0);
+        put_sums<S>(qa + d * S::LD, q, l, qs, g > 0);
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {   // the last lane has the row's sum
+          da[i] += before<1>(da[i]);
+          da[i] += before<2>(da[i]);
+          da[i] += before<4>(da[i]);
+          da[i] += before<8>(da[i]);
+        }
+        if (l == kLanes - 1) {
+          float all[S::NL];
+          get_states<S::NL>(dA + states, all);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) all[i] += da[i];
+          put_states<S::NL>(dA + states, all);
         }
       }
-      put_sums<S>(ux + d * S::LD, q, l, gb);
-      put_sums<S>(qa + d * S::LD, q, l, qs);
+      // the waves' dB and dC, added up in their order in the places of B and C
+#pragma unroll 1
+      for (int v = 0; v < S::NW; ++v) {
+        __syncthreads();
+        if (wave != v) continue;
 #pragma unroll
-      for (int i = 0; i < S::NL; ++i) {   // the last lane has the row's sum
-        da[i] += before<1>(da[i]);
-        da[i] += before<2>(da[i]);
-        da[i] += before<4>(da[i]);
-        da[i] += before<8>(da[i]);
-      }
-      if (l == kLanes - 1) {
-        float all[S::NL];
-        get_states<S::NL>(dA + d * S::N + q * S::NL, all);
+        for (int r = 0; r < S::R; ++r) {
+          const int at = ((g * 4 + q) * S::R + r) * S::STEP + l * S::NL;
+          if (v > 0) {
+            float x[S::NL];
+            get_states<S::NL>(Bs + at, x);
 #pragma unroll
-        for (int i = 0; i < S::NL; ++i) all[i] += da[i];
-        put_states<S::NL>(dA + d * S::N + q * S::NL, all);
-      }
-    }
-    // the waves' dB and dC, added up in their order in the places of B and C
+            for (int i = 0; i < S::NL; ++i) dB[r][i] += x[i];
+            get_states<S::NL>(Cs + at, x);
 #pragma unroll
-    for (int v = 0; v < S::NW; ++v) {
-      __syncthreads();
-      if (wave != v) continue;
-#pragma unroll
-      for (int r = 0; r < S::R; ++r) {
-        float* const pB = Bs + mine_at + r * kLanes * S::NL;
-        float* const pC = Cs + mine_at + r * kLanes * S::NL;
-        if (v > 0) {
-          float x[S::NL];
-          get_states<S::NL>(pB, x);
-#pragma unroll
-          for (int i = 0; i < S::NL; ++i) dB[r][i] += x[i];
-          get_states<S::NL>(pC, x);
-#pragma unroll
-          for (int i = 0; i < S::NL; ++i) dC[r][i] += x[i];
+            for (int i = 0; i < S::NL; ++i) dC[r][i] += x[i];
+          }
+          put_states<S::NL>(Bs + at, dB[r]);
+          put_states<S::NL>(Cs + at, dC[r]);
         }
-        put_states<S::NL>(pB, dB[r]);
-        put_states<S::NL>(pC, dC[r]);
       }
     }
     __syncthreads();
+    const Pieces<S> me(tid);
+    const int c = me.c;
+    const float* const skip = tables[0] + c;
+    const float* const bias = tables[1] + c;
     float* const bc = ws.bc + ((b * blocks_of<S::DW>(a.D, a.G) + w.block) * a.T + t0) * 2 * a.N;
-    for (int i = tid; i < S::TB * 2 * S::N / 2; i += S::NT) {   // two adjacent states
+    for (int i = me.tid; i < S::TB * S::N; i += S::NT) {   // two adjacent states
       const int t = i / S::N, e = i % S::N * 2, s = e % S::N;
       if (s < a.N && t0 + t < n)
         *reinterpret_cast<float2*>(bc + (int64_t)t * 2 * a.N + (e < S::N ? 0 : a.N) + s) =
@@ -347,47 +368,58 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
     }
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
-      const int t = token(i);
-      if (t >= S::TB || !mine || t0 + t >= a.T) continue;
-      const bool in = t0 + t < n;
-      float x[8], v[8], d[8], z[8], o[3][8];
-      nx[i].get(x);
-      ndt[i].get(v);
-      ndy[i].get(d);
-      nz[i].get(z);
+      const int t = me.token(i);
+      if (t >= S::TB || c >= w.channels || t0 + t >= a.T) continue;
+      Piece r[3];
+      r[0].clear();
+      r[1].clear();
+      r[2].clear();
+      if (t0 + t < n) {
+        float x[S::PC], v[S::PC], d[S::PC], z[S::PC], o[3][S::PC];
+        Piece in[4];
+        in[0].load(a.x.p, row(me, a.x, t0 + t));
+        in[1].load(a.dt.p, row(me, a.dt, t0 + t));
+        in[2].load(a.dy.p, row(me, a.dy, t0 + t));
+        in[3].clear();
+        if (a.z.p) in[3].load(a.z.p, row(me, a.z, t0 + t));
+        in[0].get(x);
+        in[1].get(v);
+        in[2].get(d);
+        in[3].get(z);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int at = (c + e) * S::LD + S::at(t);
-        const float m = fmaf(skip[e], x[e], dm[at]), gb = ux[at], del = delta[at];
-        float g = d[e];
-        if (a.z.p) {
-          const float s = sigmoid(z[e]);
-          o[2][e] = in ? d[e] * m * (s * fmaf(z[e], 1.f - s, 1.f)) : 0.f;
-          g *= z[e] * s;
-        }
-        float ddt = fmaf(x[e], gb, qa[at] * 0.69314718f);
-        if (a.softplus) ddt *= sigmoid(v[e] + bias[e]);
-        o[0][e] = in ? fmaf(del, gb, skip[e] * g) : 0.f;
-        o[1][e] = in ? ddt : 0.f;
-        if (in) {
+        for (int e = 0; e < S::PC; ++e) {
+          const int at = (c + e) * S::LD + S::at(t);
+          const float gb = gbs[at];
+          float g = d[e];
+          if (a.z.p) {
+            const float s = sigmoid(z[e]);
+            o[2][e] = d[e] * fmaf(skip[e], x[e], ys[at]) * (s * fmaf(z[e], 1.f - s, 1.f));
+            g *= z[e] * s;
+          }
+          o[1][e] = fmaf(x[e], gb, qa[at] * 0.69314718f);
+          if (a.softplus) o[1][e] *= sigmoid(v[e] + bias[e]);
+          o[0][e] = fmaf(delta[at], gb, skip[e] * g);
           dskip[e] = fmaf(g, x[e], dskip[e]);
-          dbias[e] += ddt;
+          dbias[e] += o[1][e];
         }
+        r[0].set(o[0]);
+        r[1].set(o[1]);
+        if (a.z.p) r[2].set(o[2]);
       }
-      put8<BF>(const_cast<void*>(a.dx.p), row(a.dx, t0 + t), o[0]);
-      put8<BF>(const_cast<void*>(a.ddt.p), row(a.ddt, t0 + t), o[1]);
-      if (a.z.p) put8<BF>(const_cast<void*>(a.dz.p), row(a.dz, t0 + t), o[2]);
+      r[0].store(const_cast<void*>(a.dx.p), row(me, a.dx, t0 + t));
+      r[1].store(const_cast<void*>(a.ddt.p), row(me, a.ddt, t0 + t));
+      if (a.z.p) r[2].store(const_cast<void*>(a.dz.p), row(me, a.dz, t0 + t));
     }
-    __syncthreads();   // B and C have been read
   }
 
   // rows behind the last block's
-  if (mine) {
-    const float zero[8] = {};
-    for (int64_t t = (last + 1) * S::TB + token(0); t < a.T; t += S::NT / (S::DW / 8)) {
-      put8<BF>(const_cast<void*>(a.dx.p), row(a.dx, t), zero);
-      put8<BF>(const_cast<void*>(a.ddt.p), row(a.ddt, t), zero);
-      if (a.z.p) put8<BF>(const_cast<void*>(a.dz.p), row(a.dz, t), zero);
+  if (const Pieces<S> me(tid); me.c < w.channels) {
+    Piece zero;
+    zero.clear();
+    for (int64_t t = (last + 1) * S::TB + me.token(0); t < a.T; t += S::NT / (S::DW / S::PC)) {
+      zero.store(const_cast<void*>(a.dx.p), row(me, a.dx, t));
+      zero.store(const_cast<void*>(a.ddt.p), row(me, a.ddt, t));
+      if (a.z.p) zero.store(const_cast<void*>(a.dz.p), row(me, a.dz, t));
     }
   }
   __syncthreads();
@@ -399,17 +431,17 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
     if (a.ds_in) a.ds_in[at] = back[i];
   }
   // dD and dbias: the threads' sums of a channel in 64 bits
-  float* const join = reinterpret_cast<float*>(rows4);   // 8 floats of every thread
-  static_assert(8 * S::NT <= 4 * S::DW * S::LD, "the rows hold them");
+  float* const join = reinterpret_cast<float*>(rows4);   // S::PC floats of every thread
+  static_assert(S::PC * S::NT <= ROWS * S::DW * S::LD, "the rows hold them");
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) join[tid * 8 + e] = v ? dbias[e] : dskip[e];
+    for (int e = 0; e < S::PC; ++e) join[tid * S::PC + e] = v ? dbias[e] : dskip[e];
     __syncthreads();
     for (int d = tid; d < w.channels; d += S::NT) {
       double s = 0.0;
-      for (int i = d / 8; i < S::NT; i += S::DW / 8) s += join[i * 8 + d % 8];
+      for (int i = d / S::PC; i < S::NT; i += S::DW / S::PC) s += join[i * S::PC + d % S::PC];
       (v ? ws.bias : ws.skip)[b * a.D + w.c0 + d] = (float)s;
     }
   }
@@ -485,10 +517,10 @@ hipError_t launch(const Scan& a, void* workspace, hipStream_t s) {
 // Calls f with the instance that a call runs on.
 template <class F>
 auto with_shape(const Scan& a, F f) {
-  return a.N <= 8    ? f(Shape<2, 8, 32, 8>())
-         : a.N <= 16 ? f(Shape<4, 8, 32, 8>())
-         : a.N <= 32 ? f(Shape<8, 4, 32, 8>())
-                     : f(Shape<16, 2, 32, 8>());
+  return a.N <= 8    ? f(Shape<2, 8, 1, 32, 8, 8>())
+         : a.N <= 16 ? f(Shape<4, 4, 1, 32, 8, 4>())
+         : a.N <= 32 ? f(Shape<4, 4, 2, 32, 8, 4>())
+                     : f(Shape<4, 4, 4, 16, 8, 4>());
 }
 
 }  // namespace

@@ -259,7 +259,7 @@ def scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, le
     return out, s_out
 
 
-_STEP_TOKENS = 4   # scan calls of at most so many tokens take no workspace
+_STEP_TOKENS = 8   # scan calls of at most so many tokens take no workspace
 
 
 def scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = True, lengths=None, s_in=None,
