@@ -66,6 +66,8 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
   __shared__ float4 B4[S::TB * S::N / 4], C4[S::TB * S::N / 4];
   __shared__ float4 a4[S::DW * S::N / 4], carry4[S::DW * S::N / 4], back4[S::DW * S::N / 4], dA4[S::DW * S::N / 4];
   __shared__ float tables[2][S::DW];
+  __shared__ float4 sums4[S::NW / 2][2][S::TB * S::NS / 4];
+  float* const sums = reinterpret_cast<float*>(sums4);
   float* const delta = reinterpret_cast<float*>(rows4[0]);
   float* const ux = reinterpret_cast<float*>(rows4[1]);
   float* const dm = reinterpret_cast<float*>(rows4[2]);
@@ -251,29 +253,35 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
         Walk<S> f;
         f.run(dl, in, an, v, h0);
         asm volatile("" ::: "memory");
-        get_block<S>(Cs, g, q, l, v);
+        const int mine = ((g * 4 + q) * S::R) * S::STEP + l * S::NL;   // B and C of the lane
 #pragma unroll
         for (int r = 0; r < S::R; ++r) {
+          float Cr[S::NL];
+          get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
           y[r] = 0.f;
 #pragma unroll
           for (int i = 0; i < S::NL; ++i) {
             h[r][i] = fmaf(f.e[r][i], r ? h[r - 1][i] : f.before[i], f.u[r][i]);
-            y[r] = fmaf(v[r][i], h[r][i], y[r]);
+            y[r] = fmaf(Cr[i], h[r][i], y[r]);
             dC[r][i] = fmaf(dv[r], h[r][i], dC[r][i]);
           }
         }
+        put_sums<S>(ys + d * S::LD, q, l, y, g > 0);
+        asm volatile("" ::: "memory");
         // the adjoint that reaches the lane from the ones behind it
         float G[S::NL], P[S::NL], end[S::NL], gr[S::NL], total = f.sum;
         get_states<S::NL>(back + states, end);
 #pragma unroll
         for (int i = 0; i < S::NL; ++i) {
           G[i] = 0.f;
-#pragma unroll
-          for (int r = S::R - 1; r >= 0; --r) {
-            v[r][i] *= dv[r];   // C dm from here on
-            G[i] = f.e[r][i] * (v[r][i] + G[i]);
-          }
           P[i] = __builtin_amdgcn_exp2f(f.sum * an[i]);
+        }
+#pragma unroll
+        for (int r = S::R - 1; r >= 0; --r) {
+          float Cr[S::NL];
+          get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) G[i] = f.e[r][i] * fmaf(Cr[i], dv[r], G[i]);
         }
         const auto join = [&](auto step) {
           constexpr int K = decltype(step)::value;
@@ -293,7 +301,6 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
           gr[i] = behind_or(G[i], end[i]);
         }
         if (l == 0) put_states<S::NL>(back + states, G);
-        put_sums<S>(ys + d * S::LD, q, l, y, g > 0);
         // back over the lane's tokens
         float gb[S::R], qs[S::R], da[S::NL];
 #pragma unroll
@@ -301,12 +308,13 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
         asm volatile("" ::: "memory");
 #pragma unroll
         for (int r = S::R - 1; r >= 0; --r) {
-          float Br[S::NL];
-          get_states<S::NL>(Bs + ((g * 4 + q) * S::R + r) * S::STEP + l * S::NL, Br);
+          float Br[S::NL], Cr[S::NL];
+          get_states<S::NL>(Bs + mine + r * S::STEP, Br);
+          get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
           gb[r] = qs[r] = 0.f;
 #pragma unroll
           for (int i = 0; i < S::NL; ++i) {
-            gr[i] += v[r][i];
+            gr[i] = fmaf(Cr[i], dv[r], gr[i]);
             dB[r][i] = fmaf(in[r], gr[i], dB[r][i]);
             gb[r] = fmaf(gr[i], Br[i], gb[r]);
             gr[i] *= f.e[r][i];
@@ -332,40 +340,54 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
           put_states<S::NL>(dA + states, all);
         }
       }
-      // the waves' dB and dC, added up in their order in the places of B and C
-#pragma unroll 1
-      for (int v = 0; v < S::NW; ++v) {
-        __syncthreads();
-        if (wave != v) continue;
+      // The waves' dB and dC: the upper half of the waves hand theirs to the lower,
+      // whose sums are added up in the waves' order.
+      constexpr int HALF = S::NW / 2;
+      float* const mine = sums + wave % HALF * 2 * S::TB * S::NS;
+      if (S::NG > 1) __syncthreads();   // (the group before has been read)
 #pragma unroll
-        for (int r = 0; r < S::R; ++r) {
-          const int at = ((g * 4 + q) * S::R + r) * S::STEP + l * S::NL;
-          if (v > 0) {
-            float x[S::NL];
-            get_states<S::NL>(Bs + at, x);
+      for (int step = 0; step < 2; ++step) {
+        if (wave / HALF == 1 - step)
 #pragma unroll
-            for (int i = 0; i < S::NL; ++i) dB[r][i] += x[i];
-            get_states<S::NL>(Cs + at, x);
+          for (int r = 0; r < S::R; ++r) {
+            float* const pB = mine + (q * S::R + r) * S::STEP + l * S::NL;
+            float* const pC = pB + S::TB * S::NS;
+            if (step) {
+              float x[S::NL];
+              get_states<S::NL>(pB, x);
 #pragma unroll
-            for (int i = 0; i < S::NL; ++i) dC[r][i] += x[i];
+              for (int i = 0; i < S::NL; ++i) dB[r][i] += x[i];
+              get_states<S::NL>(pC, x);
+#pragma unroll
+              for (int i = 0; i < S::NL; ++i) dC[r][i] += x[i];
+            }
+            put_states<S::NL>(pB, dB[r]);
+            put_states<S::NL>(pC, dC[r]);
           }
-          put_states<S::NL>(Bs + at, dB[r]);
-          put_states<S::NL>(Cs + at, dC[r]);
+        __syncthreads();
+      }
+      const int thread = anew(tid);
+      float* const bc = ws.bc + ((b * blocks_of<S::DW>(a.D, a.G) + w.block) * a.T + t0) * 2 * a.N;
+#pragma unroll
+      for (int i = 0; i < (8 * S::TB + S::NT - 1) / S::NT; ++i) {   // NL adjacent states of a token, of B, then of C
+        const int e = thread + i * S::NT, c = e / (4 * S::TB);
+        const int t = e % kLanes * S::R + e / kLanes % S::R, s = g * S::NS + e / S::TB % 4 * S::NL;
+        if (e >= 8 * S::TB || s >= a.N || t0 + t >= n) continue;
+        float x[S::NL], y[S::NL];
+        get_states<S::NL>(sums + e * S::NL, x);
+#pragma unroll
+        for (int v = 1; v < HALF; ++v) {
+          get_states<S::NL>(sums + v * 2 * S::TB * S::NS + e * S::NL, y);
+#pragma unroll
+          for (int k = 0; k < S::NL; ++k) x[k] += y[k];
         }
+        put_states<S::NL>(bc + ((int64_t)t * 2 + c) * a.N + s, x);
       }
     }
-    __syncthreads();
     const Pieces<S> me(tid);
     const int c = me.c;
     const float* const skip = tables[0] + c;
     const float* const bias = tables[1] + c;
-    float* const bc = ws.bc + ((b * blocks_of<S::DW>(a.D, a.G) + w.block) * a.T + t0) * 2 * a.N;
-    for (int i = me.tid; i < S::TB * S::N; i += S::NT) {   // two adjacent states
-      const int t = i / S::N, e = i % S::N * 2, s = e % S::N;
-      if (s < a.N && t0 + t < n)
-        *reinterpret_cast<float2*>(bc + (int64_t)t * 2 * a.N + (e < S::N ? 0 : a.N) + s) =
-            *reinterpret_cast<const float2*>((e < S::N ? Bs : Cs) + S::at(t, s));
-    }
 #pragma unroll
     for (int i = 0; i < S::TURNS; ++i) {
       const int t = me.token(i);
@@ -515,12 +537,19 @@ hipError_t launch(const Scan& a, void* workspace, hipStream_t s) {
 }
 
 // Calls f with the instance that a call runs on.
+template <int NL, int R, int NG, int MOST, class F>
+auto with_channels(const Scan& a, F f) {
+  if constexpr (MOST == 32)
+    if (a.B * blocks_of<32>(a.D, a.G) >= 192) return f(Shape<NL, R, NG, 32, 8, 8>());
+  if (a.B * blocks_of<16>(a.D, a.G) >= 192) return f(Shape<NL, R, NG, 16, 8, 4>());
+  return f(Shape<NL, R, NG, 8, 8, 4>());
+}
 template <class F>
 auto with_shape(const Scan& a, F f) {
-  return a.N <= 8    ? f(Shape<2, 8, 1, 32, 8, 8>())
-         : a.N <= 16 ? f(Shape<4, 4, 1, 32, 8, 4>())
-         : a.N <= 32 ? f(Shape<4, 4, 2, 32, 8, 4>())
-                     : f(Shape<4, 4, 4, 16, 8, 4>());
+  if (a.N > 32) return with_channels<4, 4, 4, 16>(a, f);
+  if (a.T <= 64)
+    return a.N <= 8 ? with_channels<2, 4, 1, 32>(a, f) : a.N <= 16 ? with_channels<4, 4, 1, 32>(a, f) : with_channels<4, 4, 2, 16>(a, f);
+  return a.N <= 8 ? with_channels<2, 8, 1, 32>(a, f) : a.N <= 16 ? with_channels<4, 8, 1, 32>(a, f) : with_channels<4, 8, 2, 16>(a, f);
 }
 
 }  // namespace
