@@ -72,7 +72,7 @@ extern "C" {
  *
  *   B, T, D, W   batch, tokens, channels (a multiple of 8 up to 2^20) and inputs
  *             of the window, 2 to SSM_MAX_WINDOW; B * D is at most 2^25 and B * (T / 16
- *             + 256) * (D / 4 + 2) below 2^32
+ *             + 258) * (D + 2) below 2^32
  *   x, y      [B, T, D] of `dtype`
  *   weight    [D, W] float32, contiguous; weight[d][W - 1] is the current token's
  *   bias      NULL (zero), or D float32 values
@@ -129,7 +129,6 @@ size_t ssm_conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t W, 
  *   strides   NULL, or 18 values: (batch, token, group) distances of x, dt, Bm,
  *             Cm, z and y (x, dt, z and y have no groups: theirs is not read)
  *   T == 0    s_out receives s_in (or zero).  B == 0: nothing is done.
- * B * T * G * N is below 2^32.
  *
  * Calls of at most 8 tokens run token by token, longer ones over blocks of 32 to
  * 128 tokens whose tokens lie side by side over lanes.

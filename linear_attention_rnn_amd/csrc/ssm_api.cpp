@@ -15,8 +15,7 @@
 namespace {
 
 // Sizes that the convolution and the scan have in common.  A launch holds fewer
-// than 2^32 work-items: 64 for each 8 channels at most, but for the scan's
-// token-by-token calls, 16 for each channel.
+// than 2^32 work-items: the scan's at most 512 for each 8 channels.
 int check_sizes(int64_t B, int64_t T, int64_t D, int dtype) {
   if (B < 0 || T < 0 || D < 1) return invalid("sizes must be B, T >= 0 and D >= 1");
   const int st = known_dtype(dtype);
@@ -39,9 +38,9 @@ int conv_sizes(int64_t B, int64_t T, int64_t D, int64_t W, int dtype) {
   int st = check_sizes(B, T, D, dtype);
   if (st != WKV6_OK) return st;
   if (W < 2 || W > SSM_MAX_WINDOW) return unsupported("W must be from 2 to 4");
-  // 8 channels and a run of at least 16 tokens for each thread; workgroups hold
+  // 2 channels and a run of at least 16 tokens for each thread; workgroups hold
   // up to 256 runs, and up to twice the channels there are
-  return check_items(B, T / 16 + 256, D / 4 + 2);
+  return check_items(B, T / 16 + 258, D + 2);
 }
 
 ssm::Conv conv_args(int64_t B, int64_t T, int64_t D, int64_t W, const float* weight, const float* bias, int act,
@@ -78,7 +77,7 @@ int scan_sizes(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int dtype)
   if (G < 1) return invalid("G must be at least 1");
   if (D % G || D / G % 8) return unsupported("D must be a multiple of 8 G");
   if (N < 8 || N > SSM_MAX_STATES || N % 8) return unsupported("N must be a multiple of 8 from 8 to 64");
-  return check_items(B, T, G * N);
+  return WKV6_OK;
 }
 
 ssm::Scan scan_args(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int dtype) {

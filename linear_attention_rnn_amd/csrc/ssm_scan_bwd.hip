@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "ssm_scan.h"
@@ -469,33 +470,46 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
   }
 }
 
-// dB and dC: the blocks' sums, in 64 bits; zero where no token counts.
+// dB and dC: the blocks' sums, in 64 bits; zero where no token counts.  A workgroup
+// has 16 pairs of adjacent states and the blocks in 16 interleaved shares.
 template <bool BF>
 __global__ __launch_bounds__(256) void bc_sum_kernel(Scan a, const float* bc, int per) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;   // over [B, G, T, 2, N / 2]
-  const int pairs = a.N / 2;
-  const int s = (int)(id % pairs) * 2;
-  const int c = (int)(id / pairs % 2);
-  const int64_t t = id / (2 * pairs) % a.T, bg = id / (2 * pairs) / a.T;
-  if (bg >= a.B * a.G) return;
-  const int64_t b = bg / a.G;
-  const int g = (int)(bg % a.G);
-  double x = 0.0, y = 0.0;
-  if (t < tokens_of(a.lengths, b, a.T)) {
-    const float* p = bc + (bg * per * a.T + t) * 2 * a.N + c * a.N + s;
-#pragma unroll 8
-    for (int i = 0; i < per; ++i) {
-      const float2 f = *reinterpret_cast<const float2*>(p + (int64_t)i * a.T * 2 * a.N);
-      x += f.x;
-      y += f.y;
+  __shared__ double lds[16][32 + 1];
+  const int pairs = a.N / 2, share = threadIdx.x / 16, at = threadIdx.x % 16;
+  const int64_t all = a.B * a.G * a.T * a.N;
+  for (int64_t first = (int64_t)blockIdx.x * 16; first < all; first += (int64_t)gridDim.x * 16) {
+    const int64_t id = first + at;   // over [B, G, T, 2, N / 2]
+    const int s = (int)(id % pairs) * 2, c = (int)(id / pairs % 2);
+    const int64_t t = id / (2 * pairs) % a.T, bg = id / (2 * pairs) / a.T;
+    const bool live = id < all;
+    double x = 0.0, y = 0.0;
+    if (live && t < tokens_of(a.lengths, bg / a.G, a.T)) {
+      const float* p = bc + (bg * per * a.T + t) * 2 * a.N + c * a.N + s;
+#pragma unroll 4
+      for (int i = share; i < per; i += 16) {
+        const float2 f = *reinterpret_cast<const float2*>(p + (int64_t)i * a.T * 2 * a.N);
+        x += f.x;
+        y += f.y;
+      }
     }
+    __syncthreads();   // (the pairs before have been added up)
+    lds[share][2 * at] = x;
+    lds[share][2 * at + 1] = y;
+    __syncthreads();
+    if (share || !live) continue;
+    x = y = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x += lds[i][2 * at];
+      y += lds[i][2 * at + 1];
+    }
+    const Tensor& to = c ? a.dc : a.db;
+    const int64_t out = bg / a.G * to.b + t * to.t + bg % a.G * to.h + s;
+    if constexpr (BF)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(const_cast<void*>(to.p)) + out) = linattn::pair((float)x, (float)y);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(const_cast<void*>(to.p)) + out) = make_float2((float)x, (float)y);
   }
-  const Tensor& to = c ? a.dc : a.db;
-  const int64_t at = b * to.b + t * to.t + g * to.h + s;
-  if constexpr (BF)
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(const_cast<void*>(to.p)) + at) = linattn::pair((float)x, (float)y);
-  else
-    *reinterpret_cast<float2*>(static_cast<float*>(const_cast<void*>(to.p)) + at) = make_float2((float)x, (float)y);
 }
 
 // dA, dD and dbias: the batch items' sums.
@@ -528,7 +542,7 @@ hipError_t launch(const Scan& a, void* workspace, hipStream_t s) {
                        dim3((unsigned)grid_of<S::DW>(a)), dim3(S::NT), 0, s, a, ws, lay.blocks);
     const int64_t pairs = a.B * a.G * a.T * a.N;
     if (pairs)
-      hipLaunchKernelGGL((a.bf16 ? bc_sum_kernel<true> : bc_sum_kernel<false>), dim3((unsigned)((pairs + 255) / 256)),
+      hipLaunchKernelGGL((a.bf16 ? bc_sum_kernel<true> : bc_sum_kernel<false>), dim3((unsigned)std::min<int64_t>((pairs + 15) / 16, 1 << 20)),
                          dim3(256), 0, s, a, ws.bc, (int)(blocks_of<S::DW>(a.D, a.G) / a.G));
   }
   const int64_t all = (int64_t)a.D * (a.N + 2);

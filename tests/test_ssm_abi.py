@@ -118,7 +118,7 @@ ROWS = [*CHANNELS, *CHANNELS, *STATES, *STATES, *CHANNELS, *CHANNELS]
 SIZES = [(dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(D=0), INVALID), (dict(G=0), INVALID), (dict(dtype=7), INVALID),
          (dict(D=60), UNSUPPORTED), (dict(G=3), UNSUPPORTED), (dict(G=16), UNSUPPORTED), (dict(N=0), UNSUPPORTED),
          (dict(N=12), UNSUPPORTED), (dict(N=72), UNSUPPORTED), (dict(B=2 ** 20), UNSUPPORTED), (dict(B=2 ** 60), UNSUPPORTED),
-         (dict(T=2 ** 31), UNSUPPORTED), (dict(T=2 ** 27), UNSUPPORTED),
+         (dict(T=2 ** 31), UNSUPPORTED),
          *((dict([(n, 0)]), INVALID) for n in ("x", "dt", "A", "Bm", "Cm")),
          *((dict([(n, P(i) + 4)]), MISALIGNED) for i, n in enumerate(SCAN))]
 
