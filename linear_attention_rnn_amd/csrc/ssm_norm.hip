@@ -143,9 +143,11 @@ Units units_of(const BlockNorm& a) {
   Units u;
   const bool shared = a.gate && a.gate_rows > 1;
   u.span = shared ? a.gate_rows : a.rows;
-  // Two workgroups for each CU where there are rows for them.
+  // Two workgroups for each CU where there are rows for them, one of eight waves
+  // (us, one / two: 2048 rows of 8192 columns 76.5 / 88.5, 1024 of 16384 99 / 124;
+  // 16384 of 1024, four waves, 75 / 51).
   const int tpr = shape_of(a.C, true).tpr, side = tpr >= 256 ? 1 : 256 / tpr;
-  const int64_t turns = (a.rows + 512 * side - 1) / (512 * side);
+  const int64_t all = (tpr >= 512 ? 256 : 512) * side, turns = (a.rows + all - 1) / all;
   u.rows = (int)(turns < 1 ? 1 : turns > kUnitRows ? kUnitRows : turns) * side;
   u.per = u.span ? (u.span + u.rows - 1) / u.rows : 0;
   u.units = u.span ? a.rows / u.span * u.per : 0;
@@ -170,6 +172,24 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dpost[v][j] = dpre[v][j] = dgate[v][j] = 0.f;
+  // Both weights stay in registers up to two pieces a thread: read again for every
+  // row they are two thirds of what comes through the first-level cache (16384 x
+  // 1024 bfloat16 with a gate for each sequence, us, 61.0 / 51.5).  With four pieces
+  // they would spill.
+  constexpr bool HELD = NV <= 2;
+  float wpost[HELD ? NV : 1][8], wpre[HELD ? NV : 1][8];
+  const auto weight = [&](const float* from, int v, float(&q)[8]) {
+    const int c = (v * TPR + at) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = 1.f;
+    if (from && c < a.C) get8<false>(from, c, q);
+  };
+  if constexpr (HELD)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      weight(a.post, v, wpost[v]);
+      weight(a.pre, v, wpre[v]);
+    }
   // every wave of a workgroup makes the same turns where rows are shared by waves (RW == 1)
   int turn = 0;
   for (int64_t row = begin + slot; row < end; row += RW, turn ^= 1) {
@@ -199,7 +219,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;
       rd[v].get(H[v]);
-      float x[8], h[8], d[8], q[8];
+      float x[8], h[8], d[8];
       if (a.post) {
         rx[v].get(x);
 #pragma unroll
@@ -208,11 +228,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
       if (a.pre && c < a.C) {
         rh[v].get(h);
         ry[v].get(d);
-        get8<false>(a.pre, c, q);
+        if constexpr (!HELD) weight(a.pre, v, wpre[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           hh = fmaf(h[j], h[j], hh);
-          hd = fmaf(h[j], d[j] * q[j], hd);
+          hd = fmaf(h[j], d[j] * wpre[HELD ? v : 0][j], hd);
         }
       }
     }
@@ -227,28 +247,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;
       if (c >= a.C) continue;
-      float q[8], x[8];
+      float x[8];
       if (a.pre) {
         float h[8], d[8];
         rh[v].get(h);
         ry[v].get(d);
-        get8<false>(a.pre, c, q);
+        if constexpr (!HELD) weight(a.pre, v, wpre[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           dpre[v][j] = fmaf(d[j], h[j] * rp, dpre[v][j]);
-          H[v][j] = fmaf(rp, d[j] * q[j] - h[j] * f, H[v][j]);
+          H[v][j] = fmaf(rp, d[j] * wpre[HELD ? v : 0][j] - h[j] * f, H[v][j]);
         }
       }
       if (a.dresidual) put8<BF>(a.dresidual, base + c, H[v]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) H[v][j] *= a.scale;
       rx[v].get(x);
-      if (a.post) {
-        get8<false>(a.post, c, q);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = 1.f;
-      }
+      if constexpr (!HELD) weight(a.post, v, wpost[0]);
       if (a.gate) {
         float g[8], dg[8];
         rg[v].get(g);
@@ -256,7 +271,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
         for (int j = 0; j < 8; ++j) {
           float value, slope;
           act_and_slope(a.act, g[j], value, slope);
-          dg[j] = H[v][j] * (a.post ? x[j] * rq * q[j] : x[j]) * slope;
+          dg[j] = H[v][j] * (a.post ? x[j] * rq * wpost[HELD ? v : 0][j] : x[j]) * slope;
           H[v][j] *= value;
         }
         if (u.gate < 0) {
@@ -270,7 +285,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           dpost[v][j] = fmaf(H[v][j], x[j] * rq, dpost[v][j]);
-          H[v][j] *= q[j];
+          H[v][j] *= wpost[HELD ? v : 0][j];
           xd = fmaf(x[j], H[v][j], xd);
         }
     }
