@@ -192,6 +192,9 @@ struct Pieces {
   int tid, c;
   __device__ __forceinline__ explicit Pieces(int thread) : tid(ANEW ? anew(thread) : thread), c(tid % (S::DW / S::PC) * S::PC) {}
   __device__ __forceinline__ int token(int i) const { return (tid + i * S::NT) / (S::DW / S::PC); }   // from S::TB on: none
+  // The number of its pieces of B and C: from the other half of the threads on, where
+  // there are fewer pieces of either kind than threads.
+  __device__ __forceinline__ int state_piece(int i) const { return (tid ^ (S::NT / 2)) + i * S::NT; }
 };
 
 // Where a workgroup works: a batch item, a group and up to DW of its channels.

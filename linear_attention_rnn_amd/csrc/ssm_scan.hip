@@ -15,15 +15,12 @@ namespace {
 // in flight meanwhile.
 template <class S, bool AHEAD, bool BF>
 __global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
-  __shared__ float4 delta4[S::DW * S::LD / 4], ux4[S::DW * S::LD / 4], y4[S::NG > 1 ? S::DW * S::LD / 4 : 1];
-  __shared__ float4 B4[S::TB * S::N / 4], C4[S::TB * S::N / 4];
+  constexpr int BUFFERS = AHEAD ? 2 : 1;
+  __shared__ float4 delta4[BUFFERS][S::DW * S::LD / 4], ux4[BUFFERS][S::DW * S::LD / 4];
+  __shared__ float4 y4[S::NG > 1 ? BUFFERS : 1][S::NG > 1 ? S::DW * S::LD / 4 : 1];
+  __shared__ float4 B4[BUFFERS][S::TB * S::N / 4], C4[BUFFERS][S::TB * S::N / 4];
   __shared__ float4 a4[S::DW * S::N / 4], carry4[S::DW * S::N / 4];
   __shared__ float tables[2][S::DW];
-  float* const delta = reinterpret_cast<float*>(delta4);
-  float* const ux = reinterpret_cast<float*>(ux4);
-  float* const ys = S::NG > 1 ? reinterpret_cast<float*>(y4) : ux;   // the sums of C h
-  float* const Bs = reinterpret_cast<float*>(B4);
-  float* const Cs = reinterpret_cast<float*>(C4);
   float* const a2 = reinterpret_cast<float*>(a4);
   float* const carry = reinterpret_cast<float*>(carry4);
 
@@ -66,7 +63,7 @@ __global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
+      const int p = me.state_piece(i), t = S::piece_token(p), s = S::piece_state(p);
       rB[i].clear();
       rC[i].clear();
       if (p < S::BPIECES && t0 + t < n && s < a.N) {
@@ -82,9 +79,11 @@ __global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
     if (a.z.p) rz[i].load(a.z.p, row(me, a.z, t0 + me.token(i)));
   };
 
-  if (AHEAD && n) load(0);
-  for (int64_t t0 = 0; t0 < n; t0 += S::TB) {
-    if (!AHEAD) load(t0);
+  const auto stage = [&](int64_t t0, int buffer) {
+    float* const delta = reinterpret_cast<float*>(delta4[buffer]);
+    float* const ux = reinterpret_cast<float*>(ux4[buffer]);
+    float* const Bs = reinterpret_cast<float*>(B4[buffer]);
+    float* const Cs = reinterpret_cast<float*>(C4[buffer]);
     const Mine me(tid);
     const int c = me.c;
     const float* const bias = tables[1] + c;
@@ -110,7 +109,7 @@ __global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
+      const int p = me.state_piece(i), t = S::piece_token(p), s = S::piece_state(p);
       if (p >= S::BPIECES) continue;
       float x[8], y[8];
       rB[i].get(x);
@@ -126,11 +125,31 @@ __global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
         }
       }
     }
+  };
+
+  if (AHEAD && n) {
+    load(0);
+    stage(0, 0);
+    if (S::TB < n) load(S::TB);
     __syncthreads();
-    if (AHEAD) {
+  }
+  for (int64_t t0 = 0; t0 < n; t0 += S::TB) {
+    const int buffer = AHEAD ? (int)(t0 / S::TB % 2) : 0;
+    float* const delta = reinterpret_cast<float*>(delta4[buffer]);
+    float* const ux = reinterpret_cast<float*>(ux4[buffer]);
+    float* const ys = S::NG > 1 ? reinterpret_cast<float*>(y4[S::NG > 1 ? buffer : 0]) : ux;   // the sums of C h
+    float* const Bs = reinterpret_cast<float*>(B4[buffer]);
+    float* const Cs = reinterpret_cast<float*>(C4[buffer]);
+    if constexpr (AHEAD) {
+      const Mine me(tid);
 #pragma unroll
       for (int i = 0; i < S::TURNS; ++i) load_out(me, t0, i);
-      if (t0 + S::TB < n) load(t0 + S::TB);
+      if (t0 + S::TB < n) stage(t0 + S::TB, 1 - buffer);
+      if (t0 + 2 * S::TB < n) load(t0 + 2 * S::TB);
+    } else {
+      load(t0);
+      stage(t0, 0);
+      __syncthreads();
     }
 #pragma unroll 1
     for (int g = 0; g * S::NS < a.N; ++g) {

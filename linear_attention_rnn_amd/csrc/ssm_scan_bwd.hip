@@ -134,7 +134,7 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
+      const int p = me.state_piece(i), t = S::piece_token(p), s = S::piece_state(p);
       rB[i].clear();
       rC[i].clear();
       if (p >= S::BPIECES || t0 + t >= n || s >= a.N) continue;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
     }
 #pragma unroll
     for (int i = 0; i < S::BTURNS; ++i) {
-      const int p = me.tid + i * S::NT, t = S::piece_token(p), s = S::piece_state(p);
+      const int p = me.state_piece(i), t = S::piece_token(p), s = S::piece_state(p);
       if (p >= S::BPIECES) continue;
       float x[8], y[8];
       rB[i].get(x);
@@ -556,7 +556,7 @@ auto with_channels(const Scan& a, F f) {
   if constexpr (MOST == 32)
     if (a.B * blocks_of<32>(a.D, a.G) >= 192) return f(Shape<NL, R, NG, 32, 8, 8>());
   if (a.B * blocks_of<16>(a.D, a.G) >= 192) return f(Shape<NL, R, NG, 16, 8, 4>());
-  return f(Shape<NL, R, NG, 8, 8, 4>());
+  return f(Shape<NL, R, NG, 8, 8, 2>());
 }
 template <class F>
 auto with_shape(const Scan& a, F f) {
