@@ -193,7 +193,8 @@ def _run_own(s):
                               pre_weight=s["pre"], scale=c["scale"], activation=act, eps=s["eps"])
         return {"h": h} if y is None else {"y": y, "h": h}
     return ssm.block_norm_bwd(s["x"], s["h"], dy=s["dy"], dh=s["dh"], gate=s["gate"], post_weight=s["post"],
-                              pre_weight=s["pre"], scale=c["scale"], activation=act, eps=s["eps"])
+                              pre_weight=s["pre"], scale=c["scale"], activation=act, eps=s["eps"],
+                              want_residual=c["residual"])
 
 
 def _counts(s, T):
