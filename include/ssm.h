@@ -118,7 +118,7 @@ size_t ssm_conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t W, 
  *             and D / G are multiples of 8 (D up to 2^20), N a multiple of 8 up to
  *             SSM_MAX_STATES; B * D is at most 2^25
  *   x, dt, z, y   [B, T, D] of `dtype`; z may be NULL (no gate)
- *   A         [D, N] float32, contiguous: negative, the states' rates of decay.
+ *   A         [D, N] float32, contiguous: negative and finite, the states' rates of decay.
  *             Positive ones grow; exp(A times the steps of 128 tokens) has to be
  *             a finite float32.
  *   Bm, Cm    [B, T, G, N] of `dtype`
@@ -136,10 +136,7 @@ size_t ssm_conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t W, 
 int ssm_scan_fwd(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const void* x, const void* dt, const float* A,
                  const void* Bm, const void* Cm, const float* skip, const void* z, const float* dt_bias, int softplus,
                  const int32_t* lengths, const float* s_in, void* y, float* s_out, const int64_t* strides, int dtype,
-                 void* workspace, size_t workspace_bytes, void* stream);
-
-/* Workspace of an ssm_scan_fwd call (0: none, or the arguments are invalid). */
-size_t ssm_scan_fwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int dtype);
+                 void* stream);
 
 /*
  * ssm_scan_bwd -- gradients of sum(y * dy) + sum(s_out * ds_out).

@@ -184,18 +184,10 @@ int ssm_conv_bwd(int64_t B, int64_t T, int64_t D, int64_t W, const void* x, cons
   return no_memory();
 }
 
-size_t ssm_scan_fwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int dtype) try {
-  set_error(WKV6_OK, "");
-  if (scan_sizes(B, T, D, N, G, dtype) != WKV6_OK || B == 0) return 0;
-  return ssm::scan_workspace_bytes(scan_args(B, T, D, N, G, dtype));
-} catch (...) {
-  return 0;
-}
-
 int ssm_scan_fwd(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const void* x, const void* dt, const float* A,
                  const void* Bm, const void* Cm, const float* skip, const void* z, const float* dt_bias, int softplus,
                  const int32_t* lengths, const float* s_in, void* y, float* s_out, const int64_t* strides, int dtype,
-                 void* workspace, size_t workspace_bytes, void* stream) try {
+                 void* stream) try {
   set_error(WKV6_OK, "");
   int st = scan_sizes(B, T, D, N, G, dtype);
   if (st != WKV6_OK || B == 0 || (T == 0 && !s_out)) return st;
@@ -229,9 +221,7 @@ int ssm_scan_fwd(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const vo
   a.lengths = lengths;
   a.s_in = s_in;
   a.s_out = s_out;
-  Workspace ws(static_cast<hipStream_t>(stream));
-  if ((st = ws.take(workspace, workspace_bytes, ssm::scan_workspace_bytes(a))) != WKV6_OK) return st;
-  return ws.done(ssm::enqueue_scan(a, ws.p, ws.stream));
+  return finished(ssm::enqueue_scan(a, static_cast<hipStream_t>(stream)));
 } catch (...) {
   return no_memory();
 }

@@ -33,9 +33,6 @@ hipError_t enqueue_conv(const Conv& a, hipStream_t stream);
 size_t conv_bwd_workspace_bytes(const Conv& a);
 hipError_t enqueue_conv_bwd(const Conv& a, void* workspace, hipStream_t stream);
 
-// Calls of at most so many tokens run token by token.
-constexpr int kStepTokens = 8;
-
 struct Scan {
   int64_t B, T;
   int D, N, G;
@@ -56,8 +53,7 @@ struct Scan {
   float* dskip;                     // or null
   float* dbias;                     // or null
 };
-size_t scan_workspace_bytes(const Scan& a);
-hipError_t enqueue_scan(const Scan& a, void* workspace, hipStream_t stream);
+hipError_t enqueue_scan(const Scan& a, hipStream_t stream);
 size_t scan_bwd_workspace_bytes(const Scan& a);
 hipError_t enqueue_scan_bwd(const Scan& a, void* workspace, hipStream_t stream);
 

@@ -11,10 +11,29 @@ namespace {
 // ---- prompts.  A workgroup stages the steps and inputs of its channels and B
 // and C of a block of tokens in LDS, each wave goes through its share of the
 // channels, and the sums over the states come back through LDS to be gated and
-// stored by the threads that loaded the same places.  The next block's loads are
-// in flight meanwhile.
+// stored by the threads that loaded the same places (a thread overwrites only rows that
+// it has read itself, so that one barrier parts staging from the walk and one the walk from the
+// output).  AHEAD: the next block is staged into a second buffer, and the one after it loaded, before
+// a block's walk, which saves a barrier for each block and hides the loads; calls of many workgroups
+// hide them by each other.
+//
+// bf16, 16 states, gate: 8 x 4096 tokens of 2048 channels 400 us, 0.37 ps a token and state
+// (0.54 GB moved at 1.35 TB/s: bound by the vector instructions, 141 us of them if every SIMD
+// issued one each clock, exps at a quarter of the rate 215); 8192 tokens of 1536 channels 138, where
+// 192 workgroups leave a quarter of the CUs without one.
+//
+// Waves a SIMD that LDS leaves room for, up to 4, for which the registers are made to do (128 each:
+// 8 x 4096 tokens of 2048 channels 441 -> 400 us).  Two buffers leave room for one or two
+// workgroups of 8 waves, which need no such bound.
+template <class S, bool AHEAD>
+constexpr int waves_of() {
+  constexpr int floats = (S::NG > 1 ? 3 : 2) * S::DW * S::LD + 2 * S::TB * S::N + 2 * S::DW * S::N + 2 * S::DW;
+  constexpr int waves = 160 * 1024 / (4 * floats) * S::NW / 4;
+  return AHEAD ? 1 : waves < 4 ? waves : 4;
+}
+
 template <class S, bool AHEAD, bool BF>
-__global__ __launch_bounds__(S::NT, AHEAD ? 1 : 4) void scan_kernel(Scan a) {
+__global__ __launch_bounds__(S::NT, (waves_of<S, AHEAD>())) void scan_kernel(Scan a) {
   constexpr int BUFFERS = AHEAD ? 2 : 1;
   __shared__ float4 delta4[BUFFERS][S::DW * S::LD / 4], ux4[BUFFERS][S::DW * S::LD / 4];
   __shared__ float4 y4[S::NG > 1 ? BUFFERS : 1][S::NG > 1 ? S::DW * S::LD / 4 : 1];
@@ -319,18 +338,39 @@ void launch(const Scan& a, hipStream_t s) {
                      dim3(S::NT), 0, s, a);
 }
 
+// Channels and waves of a workgroup, with the number of workgroups of 8 channels; us for
+// 2048 tokens of 16 states with 8 channels and two buffers by 8 waves / 8 by 4 waves / 16 by 4
+// waves:
+//   256: 35 / 59 / 87    512: 67 / 72 / 87    600: 99 / 93 / 116    1024: 150 / 121 / 127
+//   2048: 300 / 224 / 204
+// Up to two workgroups for each CU there are waves enough only with 8 of them each, and the
+// second buffer hides the staging; from there on more channels share what is staged of B and C.
+// Of 32 states the rows of 16 channels leave room for two waves a SIMD: 402 with 8 channels,
+// 410 with 16.  Of 64 states B and C of a block, 64 KB, leave one workgroup of 8 waves a CU either
+// way; 8 channels with two buffers and 32 with one: 512: 193 / 368, 1024: 385 / 386, but 64 x 48
+// tokens of 2048 channels 376 / 169.
 template <int NL, int R, int NG>
 void launch_blocks(const Scan& a, hipStream_t s) {
-  const int64_t groups = a.B * blocks_of<8>(a.D, a.G);   // of 8 channels
-  if (NG == 4 ? groups < 1024 : groups < 400)
-    launch<Shape<NL, R, NG, 8, 8, 4>, true>(a, s);
-  else if constexpr (NG == 4)
+  const int64_t groups = a.B * blocks_of<8>(a.D, a.G);
+  if (groups <= (NG == 4 ? 1024 : 512)) return launch<Shape<NL, R, NG, 8, 8, 4>, true>(a, s);
+  if constexpr (NG == 4) {
     launch<Shape<NL, R, NG, 32, 8, 8>, false>(a, s);
-  else if (NG == 2 || groups < 1024)
+  } else if constexpr (NG == 2) {
     launch<Shape<NL, R, NG, 8, 4, 4>, false>(a, s);
-  else
-    launch<Shape<NL, R, NG, 16, 4, 8>, false>(a, s);
+  } else {
+    if (groups <= 1024)
+      launch<Shape<NL, R, NG, 8, 4, 4>, false>(a, s);
+    else
+      launch<Shape<NL, R, NG, 16, 4, 8>, false>(a, s);
+  }
 }
+
+// Up to so many tokens go token by token.  Either way with 64 x 2048 channels: 8 tokens 16.0 us,
+// by blocks 36.8; 10 tokens 19.5 / 37.0; but 1 x 2048 channels, 10 tokens: 11.2 / 9.4, 16 tokens: 16.4 / 9.5.
+constexpr int kTokens = 8;
+
+// Tokens of a block are 16 R: 64 x 32 tokens of 2048 channels with R of 2, 4 and 8 38 / 51 / 83 us,
+// of 64 tokens with 4 and 8 53 / 85; prompts of 8 x 4096 tokens with 4 and 8 507 / 400.
 template <int R>
 void launch_tokens(const Scan& a, hipStream_t s) {
   (a.N <= 8 ? launch_blocks<2, R, 1> : a.N <= 16 ? launch_blocks<4, R, 1> : a.N <= 32 ? launch_blocks<4, R, 2> : launch_blocks<4, R, 4>)(a, s);
@@ -338,10 +378,8 @@ void launch_tokens(const Scan& a, hipStream_t s) {
 
 }  // namespace
 
-size_t scan_workspace_bytes(const Scan&) { return 0; }
-
-hipError_t enqueue_scan(const Scan& a, void*, hipStream_t s) {
-  if (a.T <= kStepTokens)
+hipError_t enqueue_scan(const Scan& a, hipStream_t s) {
+  if (a.T <= kTokens)
     (a.N <= 8 ? launch_steps<1> : a.N <= 16 ? launch_steps<2> : a.N <= 32 ? launch_steps<4> : launch_steps<8>)(a, s);
   else
     (a.T <= 32 ? launch_tokens<2> : a.T <= 64 ? launch_tokens<4> : launch_tokens<8>)(a, s);

@@ -5,7 +5,7 @@ Argument marshalling only, as in ``linear_attention_rnn_amd.linattn``: every
 computation runs in the library's HIP kernels, PyTorch provides device memory
 and the current HIP stream, and there is no fallback.  Calls run on the inputs'
 GPU whichever device is current.  Workspaces, streams and graphs are as in
-``linattn``: calls on torch's current stream take their workspace from torch's
+``linattn``: gradients on torch's current stream take their workspace from torch's
 allocator and can be captured; calls with a ``stream`` of their own take it
 from the library's pool, or are given a ``workspace``, a uint8 tensor of at
 least ``*_workspace_bytes`` bytes, to be recorded.
@@ -17,7 +17,7 @@ import ctypes
 import torch
 
 from . import linattn, wkv6
-from .linattn import _DTYPES, _NO_WORKSPACE, _call, _dtype, _flat, _workspace
+from .linattn import _DTYPES, _call, _dtype, _flat, _workspace
 
 MAX_STATES = 64         # SSM_MAX_STATES
 MAX_WINDOW = 4          # SSM_MAX_WINDOW
@@ -38,7 +38,7 @@ def lib() -> ctypes.CDLL:
         tail = [vp, sz, vp]   # workspace, its bytes, stream
         L.ssm_conv_fwd.argtypes = [i64] * 4 + [vp] * 3 + [i32] + [vp] * 5 + [i32, vp]
         L.ssm_conv_bwd.argtypes = [i64] * 4 + [vp] * 3 + [i32] + [vp] * 9 + [i32] + tail
-        L.ssm_scan_fwd.argtypes = [i64] * 5 + [vp] * 8 + [i32] + [vp] * 5 + [i32] + tail
+        L.ssm_scan_fwd.argtypes = [i64] * 5 + [vp] * 8 + [i32] + [vp] * 5 + [i32, vp]
         L.ssm_scan_bwd.argtypes = [i64] * 5 + [vp] * 8 + [i32] + [vp] * 14 + [i32] + tail
         L.ssm_block_norm.argtypes = [i64, i64, vp, vp, vp, i64, vp, vp, f32, i32, f32, vp, vp, i32, vp]
         L.ssm_block_norm_bwd.argtypes = [i64, i64, vp, vp, vp, i64, vp, vp, f32, i32, f32] + [vp] * 7 + [i32] + tail
@@ -47,10 +47,9 @@ def lib() -> ctypes.CDLL:
                   L.ssm_block_norm_bwd, L.ssm_abi_version):
             f.restype = i32
         L.ssm_conv_bwd_workspace_bytes.argtypes = [i64] * 4 + [i32]
-        L.ssm_scan_fwd_workspace_bytes.argtypes = L.ssm_scan_bwd_workspace_bytes.argtypes = [i64] * 5 + [i32]
+        L.ssm_scan_bwd_workspace_bytes.argtypes = [i64] * 5 + [i32]
         L.ssm_block_norm_bwd_workspace_bytes.argtypes = [i64] * 3 + [i32] * 4
-        for f in (L.ssm_conv_bwd_workspace_bytes, L.ssm_scan_fwd_workspace_bytes, L.ssm_scan_bwd_workspace_bytes,
-                  L.ssm_block_norm_bwd_workspace_bytes):
+        for f in (L.ssm_conv_bwd_workspace_bytes, L.ssm_scan_bwd_workspace_bytes, L.ssm_block_norm_bwd_workspace_bytes):
             f.restype = sz
         _fns = L
     return L
@@ -63,11 +62,6 @@ def abi_version() -> int:
 def conv_bwd_workspace_bytes(B, T, D, W, dtype=torch.bfloat16) -> int:
     """Workspace bytes of a conv_bwd call of these sizes (host arithmetic)."""
     return lib().ssm_conv_bwd_workspace_bytes(B, T, D, W, _DTYPES[dtype])
-
-
-def scan_workspace_bytes(B, T, D, N, G=1, dtype=torch.bfloat16) -> int:
-    """Workspace bytes of a scan call of these sizes (host arithmetic)."""
-    return lib().ssm_scan_fwd_workspace_bytes(B, T, D, N, G, _DTYPES[dtype])
 
 
 def scan_bwd_workspace_bytes(B, T, D, N, G=1, dtype=torch.bfloat16) -> int:
@@ -230,7 +224,7 @@ def _scan(x, dt, A, B, C, D, z, dt_bias, lengths):
 
 
 def scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, lengths=None, s_in=None,
-         want_state: bool = False, out=None, s_out=None, workspace=None, stream=None):
+         want_state: bool = False, out=None, s_out=None, stream=None):
     """Selective scan of each channel d over N states: (y, s_out).
 
     delta_t = softplus(dt_t + dt_bias)  (or the sum itself),
@@ -252,14 +246,9 @@ def scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, le
     ps = _table(s_in, "s_in", (b, d, N), dev)
     s_out, po = _state_out(s_out, s_in, ps, want_state, (b, d, N), torch.float32, dev)
     L = lib()
-    pws, nws, keep = _NO_WORKSPACE if T <= _STEP_TOKENS else _workspace(
-        workspace, lambda: L.ssm_scan_fwd_workspace_bytes(b, T, d, N, G, dtype), dev, stream)
     _call("ssm_scan_fwd", L.ssm_scan_fwd, dev, stream, b, T, d, N, G, *p, softplus, pl, ps, py, po,
-          _strides(3, x, dt, B, C, z, out), dtype, pws, nws)
+          _strides(3, x, dt, B, C, z, out), dtype)
     return out, s_out
-
-
-_STEP_TOKENS = 8   # scan calls of at most so many tokens take no workspace
 
 
 def scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = True, lengths=None, s_in=None,

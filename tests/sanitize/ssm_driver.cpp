@@ -35,7 +35,7 @@ int conv_bwd(int64_t B, int64_t T, int64_t D, int64_t W, const int64_t* s = null
 }
 int scan(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const int64_t* s = nullptr) {
   return ssm_scan_fwd(B, T, D, N, G, P(0), P(1), F(2), P(3), P(4), F(5), P(6), F(7), 1, nullptr, F(8), P(9), F(10), s, 1,
-                      ws, sizeof(ws), nullptr);
+                      nullptr);
 }
 int scan_bwd(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, const int64_t* s = nullptr) {
   return ssm_scan_bwd(B, T, D, N, G, P(0), P(1), F(2), P(3), P(4), F(5), P(6), F(7), 1, nullptr, F(8), P(9), F(10), P(11),
@@ -79,7 +79,6 @@ int main() {
         }
         expect(g_ssm_enqueued - enqueued <= good, "refused calls enqueue nothing", __LINE__);
         ssm_conv_bwd_workspace_bytes(a, b, c, 4, 1);
-        ssm_scan_fwd_workspace_bytes(a, b, c, 16, 1, 1);
         ssm_scan_bwd_workspace_bytes(a, b, 64, 16, c, 1);
         ssm_block_norm_bwd_workspace_bytes(a, b, c, 1, 1, 1, 1);
       }

@@ -278,3 +278,21 @@ def test_many_channels(ssm, D):
         y2, s2 = ssm.scan(**part, want_state=True)
         torch.cuda.synchronize()
         assert bits(y[..., c:c + 8], y2) and bits(s[:, c:c + 8], s2)
+
+
+# B, D, G: 408 and 1032 workgroups of 8 channels, more than a chip holds at once, with parts of the last blocks of 16 and 32
+# channels left over; T: blocks of 32, 64 and 128 tokens
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("T", [20, 50, 133])
+@pytest.mark.parametrize("B,D,G", [(8, 408, 1), (4, 2064, 2)])
+def test_wide(ssm, B, D, G, T, N, dtype):
+    p = S.inputs(T + N, B, T, D, N, G, dtype)
+    lengths = [T, T - 3, 0, 17] * (B // 4)
+    dy, ds = normal(generator(5), B, T, D, std=1.0, dtype=p["x"].dtype), normal(generator(6), B, D, N, std=0.3)
+    q, n = S.cuda(p), torch.tensor(lengths, dtype=torch.int32).cuda()
+    y, s = ssm.scan(**q, lengths=n, want_state=True)
+    g = ssm.scan_bwd(**q, dy=dy.cuda(), ds_out=ds.cuda(), lengths=n, want_ds_in=True)
+    torch.cuda.synchronize()
+    S.check_scan(f"{B}x{T}x{D} N{N} G{G} {dtype}", p, y, s, lengths)
+    S.check_scan_bwd(f"{B}x{T}x{D} N{N} G{G} {dtype}", p, g, dy, ds, lengths)

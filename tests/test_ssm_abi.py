@@ -35,7 +35,7 @@ def test_exports_and_version():
         text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
     names = set(re.findall(r"^\s*(?:int|size_t)\s+(ssm_\w+)\s*\(", text, flags=re.M))
     assert names == {"ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_bwd_workspace_bytes", "ssm_scan_fwd",
-                     "ssm_scan_fwd_workspace_bytes", "ssm_scan_bwd", "ssm_scan_bwd_workspace_bytes", "ssm_block_norm",
+                     "ssm_scan_bwd", "ssm_scan_bwd_workspace_bytes", "ssm_block_norm",
                      "ssm_block_norm_bwd", "ssm_block_norm_bwd_workspace_bytes", "ssm_abi_version"}
     for n in names:
         assert ctypes.cast(getattr(ssm.lib(), n), ctypes.c_void_p).value
@@ -98,10 +98,10 @@ def test_conv_without_work():
 SCAN = ("x", "dt", "A", "Bm", "Cm", "skip", "z", "dt_bias", "lengths", "s_in")
 
 
-def scan(B=2, T=9, D=64, N=16, G=2, dtype=1, strides=None, ws=(0, 0), **p):
+def scan(B=2, T=9, D=64, N=16, G=2, dtype=1, strides=None, **p):
     q = pointers(SCAN + ("y", "s_out"), p)
     a = [q[n] for n in SCAN]
-    return ssm.lib().ssm_scan_fwd(B, T, D, N, G, *a[:8], 1, *a[8:], q["y"], q["s_out"], strides_of(strides), dtype, *ws, 0)
+    return ssm.lib().ssm_scan_fwd(B, T, D, N, G, *a[:8], 1, *a[8:], q["y"], q["s_out"], strides_of(strides), dtype, 0)
 
 
 GRADS = ("dy", "ds_out", "dx", "ddt", "dA", "dB", "dC", "dskip", "dz", "ddt_bias", "ds_in")
@@ -192,7 +192,6 @@ def test_norm_without_rows():
 def test_workspace_bytes():
     assert ssm.conv_bwd_workspace_bytes(-1, 4, 64, 4) == 0 and ssm.conv_bwd_workspace_bytes(2, 100, 64, 4) >= 5 * 64 * 4
     assert ssm.scan_bwd_workspace_bytes(2, 100, 64, 12) == 0 and ssm.scan_bwd_workspace_bytes(2, 100, 64, 16) >= 2 * 64 * 16 * 4
-    assert ssm.scan_workspace_bytes(2, 3, 64, 16) == 0 and ssm.scan_workspace_bytes(2, 100, 60, 16) == 0
     assert ssm.block_norm_bwd_workspace_bytes(10, 60) == 0
     assert ssm.block_norm_bwd_workspace_bytes(10, 64, 1, False, True, False) == 0   # a gate for every row needs no sums
     assert ssm.block_norm_bwd_workspace_bytes(10, 64, 5, False, True, False) >= 2 * 64 * 4
