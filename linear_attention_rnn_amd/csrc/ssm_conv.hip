@@ -4,7 +4,10 @@
 //   p_t = bias + sum_j w_j x_{t-W+1+j},  y = silu(p) or p
 //   dp = dy silu'(p),  dx_t = sum_j w_j dp_{t+W-1-j},  dw_j = sum_t dp_t x_{t-W+1+j}
 //
-// where the rows before the first token are those of the state.
+// where the rows before the first token are those of the state.  Bound by the bytes
+// of x and y (and dy and dx), read once but for the rows in front of each run: 8 x 4096
+// tokens of 2048 channels of bfloat16 55 us, 4.9 TB/s; gradients of 4 x 4096 56 us, 3.6
+// TB/s (the activation's slope is as long a wait for the vector unit).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -290,15 +293,18 @@ __global__ __launch_bounds__(256) void conv_sum_kernel(const float* part, float*
 // / 2, 4 x 4096 tokens 90.3 / 61.7 / 56.6, float32 121 / 96.9 / 90.7.
 constexpr int kPiece = 4, kPieceBwd = 2;
 
+// Runs of 16 tokens read 3 rows twice; the gradients also work those out twice, and
+// take runs of 32 once there are more than four waves for each SIMD.  Us with 16 / 32: 8 x 4096
+// tokens of 2048 channels 55.0 / 57.8, 1 x 4096 9.3 / 10.2; gradients of 1, 2 and 4 x 4096 21.5 / 22.1,
+// 35.0 / 30.1, 67.8 / 56.4.
 ConvPlan plan_of(const Conv& a, int piece) {
   ConvPlan p;
   p.pieces = a.D / piece;
   p.across = 1;
   while (p.across < 64 && p.across < p.pieces) p.across *= 2;
   p.blocks = (p.pieces + p.across - 1) / p.across;
-  p.run = 16;
   const int64_t threads = a.B * p.blocks * p.across;   // of one run
-  while (p.run < 32 && a.T > p.run && threads * (a.T / p.run) > 2 * 262144) p.run *= 2;
+  p.run = piece == kPieceBwd && threads * (a.T / 16) > 262144 ? 32 : 16;
   p.runs = a.T ? (a.T + p.run - 1) / p.run : 1;
   const int side = NTH / p.across;
   p.groups = (p.runs + side - 1) / side;

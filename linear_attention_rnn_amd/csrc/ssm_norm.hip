@@ -9,8 +9,9 @@
 //   dresidual = H,  dgate = scale act'(gate) H n  (summed over the rows that share a gate),
 //   dpost = sum scale act H x / rms(x),  dx = the post norm's gradient of scale act H post.
 //
-// Bound by the bytes of the rows, each read and written once.  A row stays in
-// registers between its sums and its outputs, laid over its threads as in the
+// Bound by the bytes of the rows, each read and written once: 32768 rows of 2048 with
+// a gate for each, bfloat16, 122 us, 5.5 TB/s; gradients of 16384 x 1024 with a gate for
+// each sequence 51 us, 3.9 TB/s.  A row stays in registers between its sums and its outputs, laid over its threads as in the
 // norms of the linear-attention layer: TPR threads, NV pieces of 8 columns each.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -112,14 +113,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   }
 }
 
-// Threads of a row and its pieces a thread, as in the norms of the
-// linear-attention layer.
+// Threads of a row and its pieces a thread.  A row of one wave needs no exchange
+// through LDS: up to two pieces a thread (us, one wave / four: 32768 rows of 1024 columns 64 /
+// 79, of 768 47 / 74; gradients of 16384 of 1024 51 / 118), not four (32768 of 2048 131 / 122,
+// gradients of 16384 of 2048 158 / 132).  Wider ones by four waves up to 4096 columns (four
+// / eight: 32768 of 4096 244 / 268, gradients of 8192 of 4096 112 / 165), by eight up to 8192
+// (four / eight: 8192 of 8192 133 / 124, gradients of 4096 184 / 137; sixteen: 126), then by
+// sixteen, the gradients, whose sums fill the registers, by eight.
 struct Shape {
   int tpr, nv;
 };
 Shape shape_of(int64_t C, bool back) {
   const int64_t pieces = C / 8;
-  const int tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= (back ? 128 : 64) ? 64 : pieces <= 512 ? 256 : pieces <= 1024 || back ? 512 : 1024;
+  const int tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 128 ? 64 : pieces <= 512 ? 256 : pieces <= 1024 || back ? 512 : 1024;
   const int64_t need = (pieces + tpr - 1) / tpr;
   return {tpr, need <= 1 ? 1 : need <= 2 ? 2 : 4};
 }
@@ -394,7 +400,7 @@ hipError_t enqueue_block_norm(const BlockNorm& a, hipStream_t s) {
   const auto go = f.tpr == 8     ? launch<8, 1>
                   : f.tpr == 16  ? launch<16, 1>
                   : f.tpr == 32  ? launch<32, 1>
-                  : f.tpr == 64  ? launch<64, 1>
+                  : f.tpr == 64  ? (f.nv == 1 ? launch<64, 1> : launch<64, 2>)
                   : f.tpr == 256 ? (f.nv == 1 ? launch<256, 1> : launch<256, 2>)
                   : f.tpr == 512 ? launch<512, 2>
                                  : launch<1024, 2>;

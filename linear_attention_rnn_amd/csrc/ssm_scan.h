@@ -7,8 +7,9 @@
 // A wave holds one channel over a block of 16 R tokens: lane (q, l) = (lane /
 // 16, lane % 16) has the R tokens from l R on and the NL states from q NL on, so
 // that four lanes hold a token's states.  B and C of its tokens and states are the
-// same for every channel of a group and stay in registers while the wave goes
-// through its channels.  Per channel:
+// same for every channel of a group; they are read from LDS for each, since
+// registers for them would halve the waves (441 -> 400 us for 8 x 4096 tokens of 2048
+// channels).  Per channel:
 //   1. decays e = exp(delta A) and inputs u = delta x B of the lane, its own
 //      state H from zero, its decay P = exp(A sum delta);
 //   2. the 16 lanes' (P, H) are combined in four doubling steps within a row of
@@ -18,8 +19,11 @@
 //   3. the lane goes through its tokens again from the state in front of them.
 // Decays and inputs stay in registers between 1 and 3: 2 more instructions for
 // each token and state than a walk over the tokens, and the scan's, for 16 times
-// as many lanes.  Bound by the vector instructions: per token and state about 10
-// (an exp counts two), and about 70 per token for softplus and gate.
+// as many lanes.  Bound by the vector instructions: per token and state about 8, an
+// exp among them that takes four times as long as another one, and about 70 per token and
+// channel for softplus and gate.  A lone wave issues one in 5 to 8 clocks, four waves of a
+// SIMD one in 3: so the kernels take few registers before they save instructions.  More
+// than 16 states go group after group, whose registers are then those of 16.
 #pragma once
 
 #include "ssm_device.h"
