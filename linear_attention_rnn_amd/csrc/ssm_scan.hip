@@ -18,8 +18,8 @@ namespace {
 // hide them by each other.
 //
 // bf16, 16 states, gate: 8 x 4096 tokens of 2048 channels 400 us, 0.37 ps a token and state
-// (0.54 GB moved at 1.35 TB/s: bound by the vector instructions, 141 us of them if every SIMD
-// issued one each clock, exps at a quarter of the rate 215); 8192 tokens of 1536 channels 138, where
+// (0.54 GB moved at 1.35 TB/s: bound by the vector instructions, 12.2 a token and state with the
+// shares of softplus and gate, 290 us of them at 3 clocks each and 8.7 an exp); 8192 tokens of 1536 channels 138, where
 // 192 workgroups leave a quarter of the CUs without one.
 //
 // Waves a SIMD that LDS leaves room for, up to 4, for which the registers are made to do (128 each:

@@ -14,10 +14,10 @@
 // registers while a wave goes through its channels, then the waves add theirs up
 // in order; the workgroups' sums are added up by a second kernel.
 //
-// Bound by the vector instructions, about 25 per token and state with two exps, and 40 in
-// the way forwards, at two waves a SIMD (a state's decays, states and sums of a lane's tokens
-// fill 250 registers).  bf16, 16 states, gate: 4 x 4096 tokens of 2048 channels 832 us, 1.6 ps a
-// token and state.
+// Bound by the vector instructions, 38 per token and state (of 16, with the shares of softplus
+// and gate; a third of them in the way forwards), at two waves a SIMD: decays, inputs, states and
+// sums of a lane's tokens fill 250 registers.  bf16, 16 states, gate: 4 x 4096 tokens of 2048
+// channels 828 us, 1.5 ps a token and state; with the 35 us that add up dB and dC.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -21,7 +21,10 @@ Contents (all arithmetic in float64 on the exact input values):
                           and gate that follow the operator in a block;
 * ``linattn_oracle``   -- (imported as a module) attention with one decay per
                           head and its gradients, rotary positions,
-                          root-mean-square norm, e4m3 rounding.
+                          root-mean-square norm, e4m3 rounding;
+* ``ssm_oracle``       -- (imported as a module) the selective scan, the short
+                          causal convolution and the norms between blocks, with
+                          their gradients.
 
 Every function here is pinned by tests that do not rely on the oracle itself
 (closed forms, a hand-worked example, invariants, brute force on tiny inputs);
