@@ -274,6 +274,8 @@ def scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = 
             q[name] = 0
         else:
             g[name], q[name] = _new(g.get(name), "d" + name, shape, t, dev)
+    if not g.keys() <= {"x", "dt", "B", "C", "z", "s_in", "A", "D", "dt_bias"}:
+        raise ValueError("an output of a name that no gradient has")
     for name, shape, given in (("A", (d, N), True), ("D", (d,), D is not None), ("dt_bias", (d,), dt_bias is not None)):
         if name in g:
             raise ValueError(f"the gradient of {name} is a new tensor")
@@ -293,6 +295,15 @@ def scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = 
 
 
 # ---------------------------------------------------------------- norms between blocks
+def _leading(gate, x, rows):
+    """Refuses a gate that broadcasting would repeat over other rows of x than those
+    that follow each other: leading dimensions of x, then ones, or as many rows in a row."""
+    for i in range(len(x) + 1):
+        if gate == x[:i] + (1,) * (len(x) - i) if len(gate) == len(x) else rows == x[:i].numel():
+            return
+    raise ValueError("gate must have leading dimensions of x, and ones behind them")
+
+
 def _block(x, gate, post_weight, pre_weight, activation):
     """Sizes, type, GPU and addresses of what block_norm and its gradients have in
     common; also how many rows share a gate."""
@@ -312,6 +323,8 @@ def _block(x, gate, post_weight, pre_weight, activation):
             if left or (rows and not per):
                 raise ValueError("the rows of gate must divide those of x")
             per = max(per, 1)
+            if x.dim() > 2 and gate.shape != x.shape:
+                _leading(gate.shape[:-1], x.shape[:-1], gates)
         elif rows:
             raise ValueError("gate has no rows")
     elif act:
@@ -330,7 +343,7 @@ def block_norm(x, residual=None, gate=None, post_weight=None, pre_weight=None, s
 
     x, residual: [..., C] float32 or bfloat16, contiguous; gate: [..., C] of x's
     type, contiguous: one row for each row of x, or for each so many rows of x
-    that follow each other ([B, 1, C] for x of [B, T, C]), or for all;
+    that follow each other ([B, 1, C] or [B, C] for x of [B, T, C]), or for all;
     activation: None, "silu" or "sigmoid", of the gate; post_weight, pre_weight:
     None or float32 [C].  `h` may be x or residual (in place).
     """

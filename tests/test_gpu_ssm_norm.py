@@ -223,3 +223,17 @@ def test_graph_and_streams(ssm):
         torch.cuda.synchronize()
         for a, b, c in zip(out, want, other):
             assert bits(a, b) and bits(a, c)
+
+
+def test_gates_of_leading_dimensions(ssm):
+    """Rows counted by leading dimensions of x, with and without ones behind them: bit for bit the gate of every row."""
+    g = generator(3)
+    x = normal(g, 2, 3, 4, 64, std=1.0).cuda()
+    gate = normal(g, 2, 3, 1, 64, std=1.0).cuda()
+    want = ssm.block_norm(x, gate=gate.expand(2, 3, 4, 64).contiguous(), activation="silu")[1]
+    for small in (gate, gate[:, :, 0], gate.view(6, 64)):
+        assert bits(ssm.block_norm(x, gate=small, activation="silu")[1], want)
+    one = gate[:, :1]
+    want = ssm.block_norm(x, gate=one.expand(2, 3, 4, 64).contiguous(), activation="sigmoid")[1]
+    for small in (one.contiguous(), one[:, 0, 0].contiguous(), one[:, 0].contiguous()):
+        assert bits(ssm.block_norm(x, gate=small, activation="sigmoid")[1], want)

@@ -73,6 +73,8 @@ def test_scan_outputs_refused():
             ssm.scan_bwd(dy=Gpu(B, T, D), out={**full, **bad}, **scan_inputs())
     with pytest.raises(ValueError):
         ssm.scan_bwd(dy=Gpu(B, T, D), out=full, **scan_inputs(z=None))
+    with pytest.raises(ValueError):
+        ssm.scan_bwd(dy=Gpu(B, T, D), out={**full, "y": Gpu(B, T, D)}, **scan_inputs())
 
 
 @pytest.mark.parametrize("kw", [
@@ -86,6 +88,17 @@ def test_block_norm_refuses(kw):
         ssm.block_norm(h=Gpu(4, 16), out=Gpu(4, 16), **x)
     with pytest.raises(ValueError):
         ssm.block_norm_bwd(h=Gpu(4, 16), dy=Gpu(4, 16), out=Gpu(4, 16), residual_out=Gpu(4, 16), **x)
+
+
+@pytest.mark.parametrize("shape,gate", [((2, 3, 16), (3, 16)), ((2, 3, 16), (1, 3, 16)), ((3, 3, 16), (1, 3, 16)), ((2, 6, 16), (3, 16)),
+                                        ((2, 3, 4, 16), (2, 1, 4, 16)), ((4, 2, 16), (2, 1, 16))])
+def test_gates_that_other_rows_would_share_refused(shape, gate):
+    """Broadcasting would repeat them over rows that do not follow each other."""
+    x = Gpu(*shape)
+    with pytest.raises(ValueError):
+        ssm.block_norm(x, gate=Gpu(*gate), h=x)
+    with pytest.raises(ValueError):
+        ssm.block_norm_bwd(x, None, gate=Gpu(*gate), out=Gpu(*shape), residual_out=Gpu(*shape))
 
 
 def test_block_norm_outputs_refused():
