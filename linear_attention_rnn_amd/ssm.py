@@ -372,7 +372,8 @@ def block_norm_bwd(x, h, dy=None, dh=None, gate=None, post_weight=None, pre_weig
 
     h: of the forward call (None without pre_weight); dy: given exactly where
     pre_weight is.  `out`: where "x" goes (dy itself is fine), `residual_out`:
-    where "residual" goes (dh itself is fine).
+    where "residual" goes (dh itself is fine).  Gates and weights that no row uses
+    have gradients of zero.
     """
     rows, C, per, act, dtype, dev, pg, pp, pq = _block(x, gate, post_weight, pre_weight, activation)
     if (dy is None) != (pre_weight is None):
@@ -384,7 +385,8 @@ def block_norm_bwd(x, h, dy=None, dh=None, gate=None, post_weight=None, pre_weig
     if residual_out is not None or want_residual:
         g["residual"] = torch.empty_like(x) if residual_out is None else residual_out
     if gate is not None:
-        g["gate"] = torch.empty_like(gate)
+        # (no rows: no kernel writes it)
+        g["gate"] = torch.empty_like(gate) if rows else torch.zeros_like(gate)
     for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
         if w is not None:
             g[name] = torch.empty((C,), dtype=torch.float32, device=dev)

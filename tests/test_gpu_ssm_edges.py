@@ -1,0 +1,49 @@
+"""The ends of the selective state space layer's calls: batches without rows,
+what is not finite in the last token, gradients that it must not reach, rows of
+zeros with the smallest eps."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ssm_oracle as R
+from tests import ssm_util as S
+from tests.ssm_util import TYPES, U, bits, f64, generator, normal
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from linear_attention_rnn_amd import ssm
+
+    return ssm
+
+
+def poison():
+    """NaN in what torch's allocator hands out next."""
+    torch.cuda.synchronize()
+    junk = [torch.full((n,), NAN, device="cuda") for n in (16, 64, 128, 512, 1024, 4096) for _ in range(16)]
+    torch.cuda.synchronize()
+    del junk
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,gate", [((0, 64), (64,)), ((0, 64), (1, 64)), ((3, 0, 64), (3, 1, 64)), ((3, 0, 64), (3, 64)),
+                                        ((0, 5, 64), (1, 1, 64)), ((0, 64), (0, 64)), ((2, 0, 64), (2, 0, 64))])
+@pytest.mark.parametrize("weights", [True, False])
+def test_gates_of_no_rows(ssm, shape, gate, weights, dtype):
+    """The gradient of a gate that no row uses is zero."""
+    t = TYPES[dtype]
+    x, g = torch.ones(shape, dtype=t, device="cuda"), torch.ones(gate, dtype=t, device="cuda")
+    w = torch.ones(64, device="cuda") if weights else None
+    kw = dict(gate=g, post_weight=w, pre_weight=w, activation="silu")
+    y, h = ssm.block_norm(x, **kw)
+    poison()
+    got = ssm.block_norm_bwd(x, h, dy=y, **kw)
+    torch.cuda.synchronize()
+    assert got["x"].shape == x.shape and got["gate"].shape == g.shape and got["gate"].dtype is t
+    for n in set(got) - {"x", "residual"}:
+        assert torch.equal(got[n], torch.zeros_like(got[n])), n
