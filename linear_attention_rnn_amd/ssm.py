@@ -258,15 +258,15 @@ def scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = 
     dy: [B, T, channels] of x's type; ds_out: None or float32 [B, channels, N].
     Returns {"x", "dt", "A", "B", "C"}, "D", "z" and "dt_bias" where those are
     given, and "s_in" if `want_ds_in`.  `out`: a dict of tensors to write "x",
-    "dt", "B", "C", "z" and "s_in" to instead of new ones (slices of one buffer
-    are fine; "s_in" may be ds_out).  Expanded inputs get the gradient of every
+    "dt", "B", "C", "z" and "s_in" to instead of new ones (None: a new one; slices
+    of one buffer are fine; "s_in" may be ds_out).  Expanded inputs get the gradient of every
     place they are used at: the caller sums them.
     """
     (b, T, d, N, G), groups, t, dev, dtype, p, pl = _scan(x, dt, A, B, C, D, z, dt_bias, lengths)
     pdy = _rows(dy, "dy", x.shape, t, dev)
     state = (b, d, N)
     ps, pd = _table(s_in, "s_in", state, dev), _table(ds_out, "ds_out", state, dev)
-    g, q = dict(out) if out else {}, {}
+    g, q = {n: t for n, t in out.items() if t is not None} if out else {}, {}
     for name, shape in (("x", x.shape), ("dt", x.shape), ("B", groups), ("C", groups), ("z", x.shape)):
         if name == "z" and z is None:
             if "z" in g:
@@ -274,7 +274,7 @@ def scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = 
             q[name] = 0
         else:
             g[name], q[name] = _new(g.get(name), "d" + name, shape, t, dev)
-    if not g.keys() <= {"x", "dt", "B", "C", "z", "s_in", "A", "D", "dt_bias"}:
+    if out and not out.keys() <= {"x", "dt", "B", "C", "z", "s_in", "A", "D", "dt_bias"}:
         raise ValueError("an output of a name that no gradient has")
     for name, shape, given in (("A", (d, N), True), ("D", (d,), D is not None), ("dt_bias", (d,), dt_bias is not None)):
         if name in g:

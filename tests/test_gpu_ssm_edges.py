@@ -47,3 +47,15 @@ def test_gates_of_no_rows(ssm, shape, gate, weights, dtype):
     assert got["x"].shape == x.shape and got["gate"].shape == g.shape and got["gate"].dtype is t
     for n in set(got) - {"x", "residual"}:
         assert torch.equal(got[n], torch.zeros_like(got[n])), n
+
+
+def test_outputs_given_as_none(ssm):
+    """An output given as None is a new tensor, the state's gradient among them."""
+    p = S.cuda(S.inputs(4, 2, 20, 16, 16, 1, "f32"))
+    dy = torch.ones_like(p["x"])
+    want = ssm.scan_bwd(**p, dy=dy, want_ds_in=True)
+    got = ssm.scan_bwd(**p, dy=dy, want_ds_in=True, out={n: None for n in ("x", "dt", "B", "C", "z", "s_in")})
+    plain = ssm.scan_bwd(**p, dy=dy, out={"s_in": None})
+    torch.cuda.synchronize()
+    assert set(got) == set(want) and all(bits(got[n], want[n]) for n in want)
+    assert set(plain) == set(want) - {"s_in"}

@@ -110,3 +110,9 @@ def test_block_norm_outputs_refused():
     for kw in (dict(h=None, dy=x, pre_weight=w), dict(h=x, pre_weight=w), dict(h=x, dy=x), dict(h=x, dh=Gpu(4, 8))):
         with pytest.raises(ValueError):
             ssm.block_norm_bwd(x, out=Gpu(4, 16), residual_out=Gpu(4, 16), **kw)
+
+
+def test_unknown_outputs_refused_as_none_too():
+    full = {n: Gpu(B, T, D) for n in ("x", "dt", "z")} | {n: Gpu(B, T, G, N) for n in ("B", "C")}
+    with pytest.raises(ValueError):
+        ssm.scan_bwd(dy=Gpu(B, T, D), out={**full, "y": None}, **scan_inputs())
