@@ -220,6 +220,9 @@ __global__ __launch_bounds__(NTH) void conv_bwd_kernel(Conv a, ConvPlan p, float
 #pragma unroll
             for (int j = 0; j < W; ++j) d[k] = fmaf(w[j][k], dp[W - 1 + i - j][k], d[k]);
           }
+          if (row >= n + W - 1)
+#pragma unroll
+            for (int k = 0; k < PC; ++k) d[k] = 0.f;   // (a weight that is not finite)
           if (a.ds_out && row >= n && row - n < W - 1) {
             Raw<BF, PC> r;
             float e[PC];

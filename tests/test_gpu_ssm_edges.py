@@ -49,6 +49,30 @@ def test_gates_of_no_rows(ssm, shape, gate, weights, dtype):
         assert torch.equal(got[n], torch.zeros_like(got[n])), n
 
 
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_behind_a_sequence_are_zero(ssm, dtype, bad):
+    """Also with weights, biases and states that are not finite."""
+    B, T, D, W = 3, 70, 16, 4
+    lengths = [0, 33, 68]
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    g, t = generator(5), TYPES[dtype]
+    x, dy = (normal(g, B, T, D, std=1.0, dtype=t).cuda() for _ in range(2))
+    w, b, s = normal(g, D, W).cuda(), normal(g, D).cuda(), normal(g, B, W - 1, D, dtype=t).cuda()
+    p = S.cuda(S.inputs(3, B, T, D, 16, 1, dtype))
+    for place in ((w, (3, 1)), (b, (5,)), (s, (1, 0, 7)), (p["s_in"], (1, 2, 3)), (p["D"], (4,)), (p["A"], (6, 2))):
+        place[0][place[1]] = bad
+    outs = [ssm.conv(x, w, b, lengths=n, s_in=s)[0]]
+    for act in ("silu", None):
+        outs.append(ssm.conv_bwd(x, w, dy, bias=b, activation=act, lengths=n, s_in=s)["x"])
+    outs.append(ssm.scan(**p, lengths=n)[0])
+    grads = ssm.scan_bwd(**p, dy=dy, lengths=n)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs + [grads[m] for m in ("x", "dt", "B", "C", "z")]):
+        for k, length in enumerate(lengths):
+            assert not o[k, length:].any(), (i, k)
+
+
 def test_outputs_given_as_none(ssm):
     """An output given as None is a new tensor, the state's gradient among them."""
     p = S.cuda(S.inputs(4, 2, 20, 16, 16, 1, "f32"))
