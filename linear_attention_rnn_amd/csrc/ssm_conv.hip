@@ -181,6 +181,7 @@ __global__ __launch_bounds__(NTH) void conv_bwd_kernel(Conv a, ConvPlan p, float
       }
     };
     const int64_t last = t1 + W - 1;   // (rows of the next run's dp reach into this one)
+    const int64_t end = t1 < n ? t1 : n;   // (behind: no gradient that could meet a row that is not finite)
     load(t0);
     for (int64_t s = t0; s < last; s += kAhead) {
 #pragma unroll
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(NTH) void conv_bwd_kernel(Conv a, ConvPlan p, float
         if (s + i >= n)
 #pragma unroll
           for (int k = 0; k < PC; ++k) dp[W - 1 + i][k] = 0.f;   // (a bias that is not finite)
-        if (s + i < t1)
+        if (s + i < end)
 #pragma unroll
           for (int k = 0; k < PC; ++k) {
 #pragma unroll

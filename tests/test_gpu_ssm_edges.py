@@ -49,6 +49,45 @@ def test_gates_of_no_rows(ssm, shape, gate, weights, dtype):
         assert torch.equal(got[n], torch.zeros_like(got[n])), n
 
 
+def changed(name, got, clean, ref, ref_clean, nan):
+    """Places whose reference does not change keep their bits; with a NaN, those that it reaches are not finite."""
+    for n in got:
+        same = ref[n] == ref_clean[n]
+        a, b = (f64(t) for t in (got[n], clean[n]))
+        assert np.array_equal(a[same], b[same]), f"{name}: d{n}"
+        if nan:
+            assert not np.isfinite(a[~np.isfinite(ref[n])]).any(), f"{name}: d{n}"
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("activation", ["silu", None])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("name", ["x", "dy"])
+def test_conv_gradients_that_nan_reaches(ssm, name, W, activation, bad):
+    """The same for the convolution, padded: the tokens behind the last one have no gradients that could meet it."""
+    B, T, D = 2, 60, 16
+    lengths = [60, 37]
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    g = generator(W)
+    p = {"x": normal(g, B, T, D, std=1.0), "weight": normal(g, D, W), "bias": normal(g, D), "s_in": normal(g, B, W - 1, D),
+         "dy": normal(g, B, T, D)}
+
+    def both(p):
+        q = {k: f64(v) for k, v in p.items()}
+        with np.errstate(all="ignore"):
+            ref = R.conv_ref_backward(**q, activation=activation, lengths=lengths)
+        got = ssm.conv_bwd(**S.cuda(p), activation=activation, lengths=n, want_ds_in=True)
+        torch.cuda.synchronize()
+        return got, ref
+
+    clean, ref_clean = both(p)
+    for at in (20, 36):
+        spoiled = {k: v.clone() for k, v in p.items()}
+        spoiled[name][1, at, 5] = bad
+        got, ref = both(spoiled)
+        changed(f"{name} at {at}", got, clean, ref, ref_clean, bad != bad)
+
+
 @pytest.mark.parametrize("bad", [NAN, INF])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_behind_a_sequence_are_zero(ssm, dtype, bad):
