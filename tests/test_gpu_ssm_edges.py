@@ -59,6 +59,35 @@ def changed(name, got, clean, ref, ref_clean, nan):
             assert not np.isfinite(a[~np.isfinite(ref[n])]).any(), f"{name}: d{n}"
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [None, [200, 151]])
+@pytest.mark.parametrize("T,N", [(200, 16), (200, 40), (256, 16), (20, 8)])
+@pytest.mark.parametrize("name", ["x", "dt", "B", "C", "z", "dy"])
+def test_scan_gradients_that_nan_reaches(ssm, name, T, N, lengths, dtype):
+    """A NaN in the middle and in the last token of one sequence reaches what the formulas say and nothing else."""
+    D, G = 32, 2
+    lengths = None if lengths is None else [n * T // 200 for n in lengths]
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32).cuda()
+    p = S.inputs(2, 2, T, D, N, G, dtype)
+    p["dy"] = normal(generator(1), 2, T, D, std=1.0, dtype=p["x"].dtype)
+    ds = normal(generator(2), 2, D, N)
+
+    def both(p):
+        q = S.oracle_args({k: v for k, v in p.items() if k != "dy"})
+        with np.errstate(all="ignore"):
+            ref = R.scan_ref_backward(**q, dy=f64(p["dy"]), ds_out=f64(ds), lengths=lengths)
+        g = ssm.scan_bwd(**S.cuda(p), ds_out=ds.cuda(), lengths=n, want_ds_in=True)
+        torch.cuda.synchronize()
+        return g, ref
+
+    clean, ref_clean = both(p)
+    for at in (T // 2 + 3, (lengths or [T, T])[1] - 1):
+        bad = {k: None if v is None else v.clone() for k, v in p.items()}
+        bad[name][1, at].view(-1)[:2] = NAN
+        got, ref = both(bad)
+        changed(f"{name} at {at}", got, clean, ref, ref_clean, True)
+
+
 @pytest.mark.parametrize("bad", [NAN, INF])
 @pytest.mark.parametrize("activation", ["silu", None])
 @pytest.mark.parametrize("W", [2, 3, 4])
