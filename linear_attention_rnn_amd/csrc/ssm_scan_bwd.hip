@@ -236,133 +236,119 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
       for (int r = 0; r < S::R; ++r)
 #pragma unroll
         for (int i = 0; i < S::NL; ++i) dB[r][i] = dC[r][i] = 0.f;
-      // ENDS: the sequence ends in the block.  Steps behind it are zero, and 0 times a state that is not finite
-      // would go into dA: the state in front of them counts as zero.  That is one instruction of 38 for each
-      // token and state, which the other blocks go without (4 x 4096 tokens of 2048 channels 830 -> 826 us).
-      // Workgroups of 8 channels go one way: two took registers (1 x 4096 tokens of 1536 channels 381 / 373).
-      const auto channels = [&](auto ENDS) __attribute__((always_inline)) {
-        const int lane = anew(tid) % 64, q = lane / 16, l = lane % 16;
 #pragma unroll 1
-        for (int d = wave; d < w.channels; d += S::NW) {
-          const int states = d * S::N + g * S::NS + q * S::NL;
-          float dl[S::R], in[S::R], dv[S::R], an[S::NL], h0[S::NL], h[S::R][S::NL], v[S::R][S::NL], y[S::R];
-          get_tokens<S>(delta + d * S::LD, l, dl);
-          get_tokens<S>(ux + d * S::LD, l, in);
-          get_tokens<S>(dm + d * S::LD, l, dv);
-          get_states<S::NL>(a2 + states, an);
-          if (k == last && last > 0) {
-            get_states<S::NL>(carry + states, h0);   // left by the way forwards
-            asm volatile("" ::: "memory");           // (a load of its own: from LDS)
-          } else if (k > 0) {
-            get_states<S::NL>(start(d, k) + g * S::NS + q * S::NL, h0);
-          } else {
-            const int at = g * S::NS + q * S::NL;
-            const float* const s = a.s_in + (b * a.D + w.c0 + d) * a.N + at;
+      for (int d = wave; d < w.channels; d += S::NW) {
+        const int states = d * S::N + g * S::NS + q * S::NL;
+        float dl[S::R], in[S::R], dv[S::R], an[S::NL], h0[S::NL], h[S::R][S::NL], v[S::R][S::NL], y[S::R];
+        get_tokens<S>(delta + d * S::LD, l, dl);
+        get_tokens<S>(ux + d * S::LD, l, in);
+        get_tokens<S>(dm + d * S::LD, l, dv);
+        get_states<S::NL>(a2 + states, an);
+        if (k == last && last > 0) {
+          get_states<S::NL>(carry + states, h0);   // left by the way forwards
+        } else if (k > 0) {
+          get_states<S::NL>(start(d, k) + g * S::NS + q * S::NL, h0);
+        } else {
+          const int at = g * S::NS + q * S::NL;
+          const float* const s = a.s_in + (b * a.D + w.c0 + d) * a.N + at;
 #pragma unroll
-            for (int i = 0; i < S::NL; ++i) h0[i] = a.s_in && at + i < a.N ? s[i] : 0.f;
-          }
-          asm volatile("" ::: "memory");
-          get_block<S>(Bs, g, q, l, v);
-          Walk<S> f;
-          f.run(dl, in, an, v, h0);
-          asm volatile("" ::: "memory");
-          const int mine = ((g * 4 + q) * S::R) * S::STEP + l * S::NL;   // B and C of the lane
+          for (int i = 0; i < S::NL; ++i) h0[i] = a.s_in && at + i < a.N ? s[i] : 0.f;
+        }
+        asm volatile("" ::: "memory");
+        get_block<S>(Bs, g, q, l, v);
+        Walk<S> f;
+        f.run(dl, in, an, v, h0);
+        asm volatile("" ::: "memory");
+        const int mine = ((g * 4 + q) * S::R) * S::STEP + l * S::NL;   // B and C of the lane
 #pragma unroll
-          for (int r = 0; r < S::R; ++r) {
-            float Cr[S::NL];
-            get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
-            y[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < S::NL; ++i) {
-              h[r][i] = fmaf(f.e[r][i], r ? h[r - 1][i] : f.before[i], f.u[r][i]);
-              y[r] = fmaf(Cr[i], h[r][i], y[r]);
-              dC[r][i] = fmaf(dv[r], h[r][i], dC[r][i]);
-            }
-          }
-          put_sums<S>(ys + d * S::LD, q, l, y, g > 0);
-          asm volatile("" ::: "memory");
-          // the adjoint that reaches the lane from the ones behind it
-          float G[S::NL], P[S::NL], end[S::NL], gr[S::NL], total = f.sum;
-          get_states<S::NL>(back + states, end);
+        for (int r = 0; r < S::R; ++r) {
+          float Cr[S::NL];
+          get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
+          y[r] = 0.f;
 #pragma unroll
           for (int i = 0; i < S::NL; ++i) {
-            G[i] = 0.f;
-            P[i] = __builtin_amdgcn_exp2f(f.sum * an[i]);
-          }
-#pragma unroll
-          for (int r = S::R - 1; r >= 0; --r) {
-            float Cr[S::NL];
-            get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
-#pragma unroll
-            for (int i = 0; i < S::NL; ++i) G[i] = f.e[r][i] * fmaf(Cr[i], dv[r], G[i]);
-          }
-          const auto join = [&](auto step) {
-            constexpr int K = decltype(step)::value;
-            total += behind<K>(total);
-            add_before<-K>(G, P);
-            if constexpr (K < 8)
-#pragma unroll
-              for (int i = 0; i < S::NL; ++i) P[i] *= behind<K>(P[i]);
-          };
-          join(std::integral_constant<int, 1>());
-          join(std::integral_constant<int, 2>());
-          join(std::integral_constant<int, 4>());
-          join(std::integral_constant<int, 8>());
-#pragma unroll
-          for (int i = 0; i < S::NL; ++i) {
-            G[i] = fmaf(__builtin_amdgcn_exp2f(total * an[i]), end[i], G[i]);
-            gr[i] = behind_or(G[i], end[i]);
-          }
-          if (l == 0) put_states<S::NL>(back + states, G);
-          // back over the lane's tokens
-          const int left = (int)(n - t0 < S::TB ? n - t0 : S::TB) - l * S::R;   // of them that count
-          float gb[S::R], qs[S::R], da[S::NL];
-#pragma unroll
-          for (int i = 0; i < S::NL; ++i) da[i] = 0.f;
-          asm volatile("" ::: "memory");
-#pragma unroll
-          for (int r = S::R - 1; r >= 0; --r) {
-            float Br[S::NL], Cr[S::NL];
-            get_states<S::NL>(Bs + mine + r * S::STEP, Br);
-            get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
-            gb[r] = qs[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < S::NL; ++i) {
-              gr[i] = fmaf(Cr[i], dv[r], gr[i]);
-              dB[r][i] = fmaf(in[r], gr[i], dB[r][i]);
-              gb[r] = fmaf(gr[i], Br[i], gb[r]);
-              gr[i] *= f.e[r][i];
-              float from = r ? h[r - 1][i] : f.before[i];
-              if (ENDS && left <= r) from = 0.f;
-              const float p = gr[i] * from;
-              qs[r] = fmaf(p, an[i], qs[r]);
-              da[i] = fmaf(p, dl[r], da[i]);
-            }
-          }
-          put_sums<S>(gbs + d * S::LD, q, l, gb, g > 0);
-          put_sums<S>(qa + d * S::LD, q, l, qs, g > 0);
-#pragma unroll
-          for (int i = 0; i < S::NL; ++i) {   // the last lane has the row's sum
-            da[i] += before<1>(da[i]);
-            da[i] += before<2>(da[i]);
-            da[i] += before<4>(da[i]);
-            da[i] += before<8>(da[i]);
-          }
-          if (l == kLanes - 1) {
-            float all[S::NL];
-            get_states<S::NL>(dA + states, all);
-#pragma unroll
-            for (int i = 0; i < S::NL; ++i) all[i] += da[i];
-            put_states<S::NL>(dA + states, all);
+            h[r][i] = fmaf(f.e[r][i], r ? h[r - 1][i] : f.before[i], f.u[r][i]);
+            y[r] = fmaf(Cr[i], h[r][i], y[r]);
+            dC[r][i] = fmaf(dv[r], h[r][i], dC[r][i]);
           }
         }
-      };
-      if constexpr (S::DW == 8) {
-        channels(std::true_type());
-      } else if (n - t0 < S::TB) {
-        channels(std::true_type());
-      } else {
-        channels(std::false_type());
+        put_sums<S>(ys + d * S::LD, q, l, y, g > 0);
+        asm volatile("" ::: "memory");
+        // the adjoint that reaches the lane from the ones behind it
+        float G[S::NL], P[S::NL], end[S::NL], gr[S::NL], total = f.sum;
+        get_states<S::NL>(back + states, end);
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          G[i] = 0.f;
+          P[i] = __builtin_amdgcn_exp2f(f.sum * an[i]);
+        }
+#pragma unroll
+        for (int r = S::R - 1; r >= 0; --r) {
+          float Cr[S::NL];
+          get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) G[i] = f.e[r][i] * fmaf(Cr[i], dv[r], G[i]);
+        }
+        const auto join = [&](auto step) {
+          constexpr int K = decltype(step)::value;
+          total += behind<K>(total);
+          add_before<-K>(G, P);
+          if constexpr (K < 8)
+#pragma unroll
+            for (int i = 0; i < S::NL; ++i) P[i] *= behind<K>(P[i]);
+        };
+        join(std::integral_constant<int, 1>());
+        join(std::integral_constant<int, 2>());
+        join(std::integral_constant<int, 4>());
+        join(std::integral_constant<int, 8>());
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {
+          G[i] = fmaf(__builtin_amdgcn_exp2f(total * an[i]), end[i], G[i]);
+          gr[i] = behind_or(G[i], end[i]);
+        }
+        if (l == 0) put_states<S::NL>(back + states, G);
+        // Back over the lane's tokens.  Steps behind the sequence are zero, and 0 times a state that is not finite
+        // would go into dA: the state in front of them counts as zero.  (An instruction for each token and state,
+        // 824 -> 833 us for 4 x 4096 tokens of 2048 channels; a way of its own for the blocks in which a sequence
+        // ends took 828, but 374 as well as this for 1 x 4096 of 1536, and twice the code.)
+        const int left = (int)(n - t0 < S::TB ? n - t0 : S::TB) - l * S::R;
+        float gb[S::R], qs[S::R], da[S::NL];
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) da[i] = 0.f;
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int r = S::R - 1; r >= 0; --r) {
+          float Br[S::NL], Cr[S::NL];
+          get_states<S::NL>(Bs + mine + r * S::STEP, Br);
+          get_states<S::NL>(Cs + mine + r * S::STEP, Cr);
+          gb[r] = qs[r] = 0.f;
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) {
+            gr[i] = fmaf(Cr[i], dv[r], gr[i]);
+            dB[r][i] = fmaf(in[r], gr[i], dB[r][i]);
+            gb[r] = fmaf(gr[i], Br[i], gb[r]);
+            gr[i] *= f.e[r][i];
+            const float p = gr[i] * (left <= r ? 0.f : r ? h[r - 1][i] : f.before[i]);
+            qs[r] = fmaf(p, an[i], qs[r]);
+            da[i] = fmaf(p, dl[r], da[i]);
+          }
+        }
+        put_sums<S>(gbs + d * S::LD, q, l, gb, g > 0);
+        put_sums<S>(qa + d * S::LD, q, l, qs, g > 0);
+#pragma unroll
+        for (int i = 0; i < S::NL; ++i) {   // the last lane has the row's sum
+          da[i] += before<1>(da[i]);
+          da[i] += before<2>(da[i]);
+          da[i] += before<4>(da[i]);
+          da[i] += before<8>(da[i]);
+        }
+        if (l == kLanes - 1) {
+          float all[S::NL];
+          get_states<S::NL>(dA + states, all);
+#pragma unroll
+          for (int i = 0; i < S::NL; ++i) all[i] += da[i];
+          put_states<S::NL>(dA + states, all);
+        }
       }
       // The waves' dB and dC: the upper half of the waves hand theirs to the lower,
       // whose sums are added up in the waves' order.
