@@ -248,7 +248,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
     }
     if (a.post) xx = over_row<TPR, false>(xx, lds[turn][2]);
     const float rp = 1.f / sqrtf(hh / (float)a.C + a.eps), rq = 1.f / sqrtf(xx / (float)a.C + a.eps);
-    const float f = rp * rp * (hd / (float)a.C);
+    const float f = rp * (rp * (hd / (float)a.C));   // (rp^2 may pass the range where hd is small or zero)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
         }
     }
     float e = 0.f;
-    if (a.post) e = rq * rq * (over_row<TPR, false>(xd, lds[turn][3]) / (float)a.C);
+    if (a.post) e = rq * (rq * (over_row<TPR, false>(xd, lds[turn][3]) / (float)a.C));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + at) * 8;

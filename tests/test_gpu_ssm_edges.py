@@ -141,6 +141,27 @@ def test_rows_behind_a_sequence_are_zero(ssm, dtype, bad):
             assert not o[k, length:].any(), (i, k)
 
 
+@pytest.mark.parametrize("C", [64, 1024, 2048, 16384])
+def test_zero_rows_with_the_smallest_eps(ssm, C):
+    """A row of zeros, whose root is sqrt(eps): 1 / rms is 2^64 at most, its square no float32.  dx = scale post pre dy / eps
+    would pass the range as well, so each norm is looked at by itself: dx = weight dy / sqrt(eps), roundings as in the norm tests."""
+    eps = 2.0 ** -128
+    g = generator(C)
+    x, w, dy = torch.zeros(3, C), 1.0 + normal(g, C, std=0.3), normal(g, 3, C, std=1.0)
+    x[1] = normal(g, C, std=1.0)
+    xs, ws, dys = x.cuda(), w.cuda(), dy.cuda()
+    y, h = ssm.block_norm(xs, pre_weight=ws, eps=eps)
+    pre = ssm.block_norm_bwd(xs, h, dy=dys, pre_weight=ws, eps=eps)
+    post = ssm.block_norm_bwd(xs, None, dh=dys, post_weight=ws, eps=eps)
+    torch.cuda.synchronize()
+    q = [f64(v) for v in (x, x, dy, None)[:3]]
+    ref = R.block_norm_ref_backward(q[0], q[1], q[2], pre=f64(w), eps=eps)
+    assert np.array_equal(f64(y)[[0, 2]], np.zeros((2, C)))
+    for got in (pre["x"], post["x"]):
+        size = np.abs(ref["x"]) + R.unit(q[0], eps)[1] * np.abs(f64(w) * q[2])
+        assert np.isfinite(f64(got)).all() and (np.abs(f64(got) - ref["x"]) <= 160 * U * size).all()
+
+
 def test_outputs_given_as_none(ssm):
     """An output given as None is a new tensor, the state's gradient among them."""
     p = S.cuda(S.inputs(4, 2, 20, 16, 16, 1, "f32"))
