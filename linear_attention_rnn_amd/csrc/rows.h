@@ -40,11 +40,6 @@ struct Raw8 {
     q[0] = at[0];
     if constexpr (!BF) q[1] = at[1];
   }
-  __device__ __forceinline__ void store(void* p, int64_t i) const {
-    uint4* at = reinterpret_cast<uint4*>(static_cast<char*>(p) + i * (BF ? 2 : 4));
-    at[0] = q[0];
-    if constexpr (!BF) at[1] = q[1];
-  }
   __device__ __forceinline__ void clear() {
     q[0] = make_uint4(0, 0, 0, 0);
     if constexpr (!BF) q[1] = q[0];
