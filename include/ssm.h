@@ -16,7 +16,8 @@
  * synchronise the host and are thread-safe.  They return a WKV6_* status
  * (wkv6.h); on INVALID_ARG, UNSUPPORTED and MISALIGNED nothing is enqueued and
  * wkv6_last_error says why.  Values are not checked: NaN and infinities
- * propagate, never to an earlier token's outputs or another channel's.
+ * propagate (an infinity may become NaN on the way), never to an earlier token's
+ * outputs or another channel's; in gradients, to what the formulas derive from them.
  * Outputs must not overlap inputs or one another except where it is said
  * below.  Every result is bit-for-bit the same for the same call (no atomics).
  *
@@ -173,7 +174,8 @@ size_t ssm_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t N, 
  *
  * with means over the C columns of each row; y is the norm of h as it is stored.
  * Squares are added up in float32: rows whose sum of squares leaves its range,
- * 2^128, give n = 0 or y = 0.
+ * 2^128, give n = 0 or y = 0; squares below 2^-126 lose places and count for little
+ * or nothing next to eps.
  *
  *   rows, C   C is a multiple of 8 up to SSM_MAX_COLUMNS; at most 2^25 rows, or
  *             2^21 of more than 512 columns
@@ -213,7 +215,10 @@ int ssm_block_norm_bwd(int64_t rows, int64_t C, const void* x, const void* h, co
                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace of an ssm_block_norm_bwd call (partial sums of dpost, dpre and of a
- * gate that rows share): post, gate and pre say which of them there are. */
+ * gate that rows share): post, gate and pre say which of them there are.  The rows of
+ * each such gate are added up apart, at least C floats for each sum and gate, written and
+ * read again: with all three sums in bfloat16 three times the bytes of x where two
+ * rows share a gate, a fifth of them where 32 or more do. */
 size_t ssm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t C, int64_t gate_rows, int post, int gate, int pre,
                                           int dtype);
 

@@ -6,8 +6,9 @@
 //
 // where the rows before the first token are those of the state.  Bound by the bytes
 // of x and y (and dy and dx), read once but for the rows in front of each run: 8 x 4096
-// tokens of 2048 channels of bfloat16 55 us, 4.9 TB/s; gradients of 4 x 4096 56 us, 3.6
-// TB/s (the activation's slope is as long a wait for the vector unit).
+// tokens of 2048 channels of bfloat16 55 us, 4.9 TB/s; gradients of 4 x 4096 58 us, 3.5
+// TB/s with the second launch (the activation's slope is as long a wait for the vector unit, and runs of 32
+// tokens work out 36 of them).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

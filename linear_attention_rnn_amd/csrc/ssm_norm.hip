@@ -10,8 +10,8 @@
 //   dpost = sum scale act H x / rms(x),  dx = the post norm's gradient of scale act H post.
 //
 // Bound by the bytes of the rows, each read and written once: 32768 rows of 2048 with
-// a gate for each, bfloat16, 122 us, 5.5 TB/s; gradients of 16384 x 1024 with a gate for
-// each sequence 51 us, 3.9 TB/s.  A row stays in registers between its sums and its outputs, laid over its threads as in the
+// a gate for each, bfloat16, 123 us, 5.5 TB/s; gradients of 16384 x 1024 with a gate for
+// each sequence 53 us, 3.8 TB/s with the launch that adds up the sums.  A row stays in registers between its sums and its outputs, laid over its threads as in the
 // norms of the linear-attention layer: TPR threads, NV pieces of 8 columns each.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -180,8 +180,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_bwd_kernel(B
     for (int j = 0; j < 8; ++j) dpost[v][j] = dpre[v][j] = dgate[v][j] = 0.f;
   // Both weights stay in registers up to two pieces a thread: read again for every
   // row they are two thirds of what comes through the first-level cache (16384 x
-  // 1024 bfloat16 with a gate for each sequence, us, 61.0 / 51.5).  With four pieces
-  // they would spill.
+  // 1024 bfloat16 with a gate for each sequence, us, 61.0 / 51.5).  Four pieces, which only rows of
+  // more than 8192 columns take, spill without them already: 14 registers of bfloat16 rows, 105 of float32 ones.
   constexpr bool HELD = NV <= 2;
   float wpost[HELD ? NV : 1][8], wpre[HELD ? NV : 1][8];
   const auto weight = [&](const float* from, int v, float(&q)[8]) {

@@ -17,10 +17,10 @@ namespace {
 // a block's walk, which saves a barrier for each block and hides the loads; calls of many workgroups
 // hide them by each other.
 //
-// bf16, 16 states, gate: 8 x 4096 tokens of 2048 channels 400 us, 0.37 ps a token and state
+// bf16, 16 states, gate: 8 x 4096 tokens of 2048 channels 403 us, 0.38 ps a token and state
 // (0.54 GB moved at 1.35 TB/s: bound by the vector instructions, 12.2 a token and state with the
-// shares of softplus and gate, 290 us of them at 3 clocks each and 8.7 an exp); 8192 tokens of 1536 channels 138, where
-// 192 workgroups leave a quarter of the CUs without one.
+// shares of softplus and gate, 290 us of them at 3 clocks each and 8.7 an exp); 8192 tokens of 1536 channels 139, where
+// 192 workgroups leave a quarter of the CUs without one.  (float32, 16 channels: 8 registers are spilled.)
 //
 // Waves a SIMD that LDS leaves room for, up to 4, for which the registers are made to do (128 each:
 // 8 x 4096 tokens of 2048 channels 441 -> 400 us).  Two buffers leave room for one or two

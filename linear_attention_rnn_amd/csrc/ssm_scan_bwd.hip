@@ -14,10 +14,10 @@
 // registers while a wave goes through its channels, then the waves add theirs up
 // in order; the workgroups' sums are added up by a second kernel.
 //
-// Bound by the vector instructions, 38 per token and state (of 16, with the shares of softplus
+// Bound by the vector instructions, 39.6 per token and state (of 16, with the shares of softplus
 // and gate; a third of them in the way forwards), at two waves a SIMD: decays, inputs, states and
-// sums of a lane's tokens fill 250 registers.  bf16, 16 states, gate: 4 x 4096 tokens of 2048
-// channels 828 us, 1.5 ps a token and state; with the 35 us that add up dB and dC.
+// sums of a lane's tokens fill 256 registers; 16 channels of 17 to 32 states spill 17 to 19 of them.  bf16, 16 states,
+// gate: 4 x 4096 tokens of 2048 channels 833 us, 1.6 ps a token and state; with the 35 us that add up dB and dC.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -309,8 +309,8 @@ __global__ __launch_bounds__(S::NT) void scan_bwd_kernel(Scan a, Sums ws, int64_
         if (l == 0) put_states<S::NL>(back + states, G);
         // Back over the lane's tokens.  Steps behind the sequence are zero, and 0 times a state that is not finite
         // would go into dA: the state in front of them counts as zero.  (An instruction for each token and state,
-        // 824 -> 833 us for 4 x 4096 tokens of 2048 channels; a way of its own for the blocks in which a sequence
-        // ends took 828, but 374 as well as this for 1 x 4096 of 1536, and twice the code.)
+        // 1% of the time for 4 x 4096 tokens of 2048 channels; a way of its own for the blocks in which a sequence
+        // ends saved half of that, nothing where there are 8 channels, and was twice the code.)
         const int left = (int)(n - t0 < S::TB ? n - t0 : S::TB) - l * S::R;
         float gb[S::R], qs[S::R], da[S::NL];
 #pragma unroll
