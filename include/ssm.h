@@ -98,6 +98,9 @@ int ssm_conv_fwd(int64_t B, int64_t T, int64_t D, int64_t W, const void* x, cons
  *   dweight   [D, W] float32;  dbias: NULL, or D float32 values.  Fully
  *             overwritten (zero when nothing counts).
  *   strides   NULL, or 6 values: (batch, token) distances of x, dy and dx
+ *
+ * A weight that is not finite makes NaN of its channel's dx and ds_in also in the first
+ * and last W - 1 rows where no token's product with it counts.
  */
 int ssm_conv_bwd(int64_t B, int64_t T, int64_t D, int64_t W, const void* x, const float* weight, const float* bias,
                  int act, const int32_t* lengths, const void* s_in, const void* dy, const void* ds_out, void* dx,
